@@ -88,7 +88,11 @@ typedef enum {
   LORA_ERR_BAD_VALUES = 4        /* lora_validate only: the tables hold invalid values       */
 } lora_status;
 
-typedef enum { LORA_BF16 = 0, LORA_FP16 = 1 } lora_dtype;
+typedef enum {
+  LORA_BF16 = 0,
+  LORA_FP16 = 1,
+  LORA_E4M3 = 2 /* 8-bit tensors of lora_rmsnorm, lora_w4_project and lora_rope_append only */
+} lora_dtype;
 
 /* Bits that lora_validate writes into *d_result. */
 enum {
@@ -327,6 +331,93 @@ LORA_API lora_status lora_base_expand(const void* x, int64_t ld_x, const void* W
                                       const float* scalings, void* out, int64_t ld_out,
                                       int tok, int K, int S, int r, int rs, int nseg, int L,
                                       lora_dtype dtype, void* stream);
+
+/* ---- operators around the adapted projection ------------------------------
+ * What makes the projection's input, the projection of a base model with 4-bit
+ * weights, and what takes its q/k/v slices.  Conventions, streams and errors
+ * as above; every row of every tensor may start at any element.  e4m3 values
+ * are rounded to nearest even and saturate at 448; a NaN stays a NaN. */
+
+/* lora_rmsnorm -- the RMS norm that makes x, the residual's addition before it
+ * and its 8-bit form behind it.
+ *   h[t, c] = rn(x[t, c] + residual[t, c])                      (x itself without a residual)
+ *   v[t, c] = h[t, c] * rsqrt(sum_c h[t, c]^2 / H + eps) * (weight[c] + weight_offset)
+ *   residual_out = h;   out = rn(v);
+ *   out_scale[t] = max_c |v[t, c]| / 448;   out_q[t, c] = e4m3(v[t, c] / out_scale[t])
+ *   x, residual, residual_out, out [tok, ld_*], weight [H]   of `dtype`
+ *   out_q [tok, ld_q] e4m3, out_scale [tok] fp32
+ * residual and residual_out go together (both NULL: no residual; the same
+ * pointer and stride: in place), and so do out_q and out_scale; of out and
+ * out_q one at least is given.  out may be x, and residual_out may be x or
+ * residual, row on row; other overlaps are undefined.  The row's sum, its
+ * factor and v are fp32.  A row of zeros (or one whose scale would be below
+ * the smallest normal fp32) has scale 0 and zeros.  A row with an infinity or
+ * a NaN has a NaN scale.
+ * H > LORA_MAX_NORM_WIDTH: LORA_ERR_UNSUPPORTED. */
+#define LORA_MAX_NORM_WIDTH 65536
+LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* residual,
+                                  int64_t ld_res, void* residual_out, int64_t ld_res_out,
+                                  const void* weight, float weight_offset, float eps, void* out,
+                                  int64_t ld_out, void* out_q, int64_t ld_q, float* out_scale,
+                                  int tok, int H, lora_dtype dtype, void* stream);
+
+/* lora_w4_project -- the base projection with 4-bit weights and group scales.
+ *   out[t, n] = rn( sx[t] * sum_g s[g, n] * sum_{k in group g} x[t, k] (q[n, k] - z[g, n]) )
+ * Group g holds k in [g*group, (g+1)*group); group is 32, 64 or 128, and the
+ * last one may be short.
+ *   x        [tok, ld_x]   of `dtype` with x_dtype == dtype (sx = 1, x_scale NULL), or e4m3
+ *                          with x_dtype == LORA_E4M3 and x_scale [tok] fp32 = sx (the out_q
+ *                          and out_scale of lora_rmsnorm)
+ *   W        [N, ld_w]     ld_w in BYTES: row n holds q[n, 0..K) in 0..15, eight values to a
+ *                          little-endian 32-bit word, value i of a word at bit
+ *                          {0, 16, 4, 20, 8, 24, 12, 28}[i]; a row takes ceil(K / 32) * 16
+ *                          bytes, of which values behind K are read but not used.  16-byte
+ *                          aligned rows (W and ld_w), else LORA_ERR_UNSUPPORTED.
+ *   w_scales [G, ld_s]     s, of `dtype`, G = ceil(K / group)
+ *   w_zeros  [G, ld_s]     z, one byte each, its low four bits read; NULL: 8 everywhere
+ *   out      [tok, ld_out] of `dtype`, written (lora_expand then adds the LoRA term).
+ * Weights, and e4m3 values of x, are exact in the products; sums are fp32. */
+LORA_API lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,
+                                     const void* W, int64_t ld_w, const void* w_scales,
+                                     const uint8_t* w_zeros, int64_t ld_s, void* out,
+                                     int64_t ld_out, int tok, int K, int N, int group,
+                                     lora_dtype x_dtype, lora_dtype dtype, void* stream);
+
+/* lora_rope_append -- rotates the q and k slices and appends k and v to a paged cache.
+ * The q/k/v slices are heads of head_dim columns at the HOST offsets
+ * qkv_offsets[0..3] of qkv [tok, ld_qkv], as lora_qkv_b wrote them.  For
+ * token t, frequency i < rotary_dim/2, p = positions[axis_map[i]][t] and the
+ * pair (a, b) of a head at columns (i, i + rotary_dim/2), or (2i, 2i+1) with
+ * `interleaved`:
+ *   a' = a cos_sin[p, i] - b cos_sin[p, rotary_dim/2 + i]
+ *   b' = b cos_sin[p, i] + a cos_sin[p, rotary_dim/2 + i]
+ * Columns from rotary_dim on pass through.  With q_weight and k_weight
+ * [head_dim] each head of q and k is first normalised,
+ * x * rsqrt(sum x^2 / head_dim + eps) * (weight + weight_offset).
+ * The results are rounded once:
+ *   q_out    [tok, ld_q]         of `dtype`; may be the q slice of qkv itself
+ *   k_cache, v_cache             head h of slot s at page*strides[0] + (s % page_size)*strides[1]
+ *                                + h*strides[2], page = s / page_size: rn(k' / k_scale) and
+ *                                rn(v / v_scale); strides (HOST, elements) of each cache;
+ *                                cache_dtype is `dtype` or LORA_E4M3
+ *   slots    [tok]               the cache slot of each token; a token whose slot is negative
+ *                                or at least num_pages*page_size writes no cache entry.
+ *                                Slots of one call must differ: of equal ones any token's
+ *                                values may end up in the entry.
+ *   positions [axes, ld_pos]     clamped to [0, max_pos); axis_map (HOST, rotary_dim/2 entries
+ *                                below axes) may be NULL with one axis
+ *   cos_sin  [max_pos, rotary_dim] fp32, cosines then sines
+ * positions and slots are both int32 (index_bytes 4) or both int64 (8).
+ * The k and v slices of qkv are not changed.  head_dim > 512 or more than four
+ * axes: LORA_ERR_UNSUPPORTED. */
+LORA_API lora_status lora_rope_append(
+    const void* qkv, int64_t ld_qkv, const int32_t* qkv_offsets, int head_dim, int rotary_dim,
+    const void* positions, int64_t ld_pos, int axes, const uint8_t* axis_map,
+    const float* cos_sin, int64_t max_pos, int interleaved, const void* q_weight,
+    const void* k_weight, float weight_offset, float eps, void* q_out, int64_t ld_q,
+    void* k_cache, const int64_t* k_strides, void* v_cache, const int64_t* v_strides,
+    int64_t num_pages, int page_size, lora_dtype cache_dtype, float k_scale, float v_scale,
+    const void* slots, int index_bytes, int tok, lora_dtype dtype, void* stream);
 
 /* ---- 64-bit index tables ------------------------------------------------
  * lora_shrink_i64 / lora_expand_i64 take seg_indptr, weight_indices and

@@ -1,0 +1,215 @@
+// layer_ops.cuh -- C ABI of the operators around the adapted projection:
+// argument checks, variant selection and launches.  Included once, by
+// lora_sgmv.cu, whose helpers and counters it uses.
+#pragma once
+
+#include "rmsnorm.cuh"
+#include "rope_append.cuh"
+#include "w4.cuh"
+
+// ------------------------------------------------------------------ RMS norm
+
+namespace {
+
+template <class E, int VPT, bool AL>
+void launch_rmsnorm(const lora::RmsNormArgs& a, int T, cudaStream_t st) {
+  const int rows = std::max(1, 256 / T);
+  const unsigned grid = static_cast<unsigned>((a.tok + rows - 1) / rows);
+  lora::rmsnorm_kernel<E, VPT, AL><<<grid, dim3(T, rows), 0, st>>>(a);
+}
+
+template <class E, bool AL>
+lora_status rmsnorm(lora::RmsNormArgs a, cudaStream_t st) {
+  // a row cut at x's 16-byte boundaries may take one block more than its
+  // length; the widest rows have no thread for it and are cut at their start
+  a.follow = (a.H + 14) / 8 <= 8 * 1024;
+  const int blocks = AL ? a.H / 8 : (a.H + (a.follow ? 14 : 7)) / 8;
+  // blocks of eight a thread
+  int vpt = 1;
+  while (vpt < 8 && (blocks + vpt - 1) / vpt > (a.tok >= 148 ? 256 : 1024)) vpt *= 2;
+  const int T = round_up((blocks + vpt - 1) / vpt, 32);
+  switch (vpt) {
+    case 1: launch_rmsnorm<E, 1, AL>(a, T, st); break;
+    case 2: launch_rmsnorm<E, 2, AL>(a, T, st); break;
+    case 4: launch_rmsnorm<E, 4, AL>(a, T, st); break;
+    default: launch_rmsnorm<E, 8, AL>(a, T, st); break;
+  }
+  ++g_launches;
+  g_last_path = LORA_PATH_GENERAL;
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* residual,
+                                    int64_t ld_res, void* residual_out, int64_t ld_res_out,
+                                    const void* weight, float weight_offset, float eps, void* out,
+                                    int64_t ld_out, void* out_q, int64_t ld_q, float* out_scale,
+                                    int tok, int H, lora_dtype dtype, void* stream) {
+  if (dtype != LORA_BF16 && dtype != LORA_FP16) return LORA_ERR_UNSUPPORTED;
+  if (tok < 0 || H < 1 || ld_x < H || !(eps >= 0.f)) return LORA_ERR_INVALID_ARGUMENT;
+  if (!out && !out_q) return LORA_ERR_INVALID_ARGUMENT;
+  if ((residual != nullptr) != (residual_out != nullptr) ||
+      (out_q != nullptr) != (out_scale != nullptr))
+    return LORA_ERR_INVALID_ARGUMENT;
+  if ((residual && (ld_res < H || ld_res_out < H)) || (out && ld_out < H) || (out_q && ld_q < H))
+    return LORA_ERR_INVALID_ARGUMENT;
+  if (H > LORA_MAX_NORM_WIDTH) return LORA_ERR_UNSUPPORTED;
+  if (tok == 0) return LORA_OK;
+  if (!x || !weight) return LORA_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(x, 2) || !aligned_to(weight, 2) || !aligned_to(residual, 2) ||
+      !aligned_to(residual_out, 2) || !aligned_to(out, 2) || !aligned_to(out_scale, 4))
+    return LORA_ERR_INVALID_ARGUMENT;
+  const lora::RmsNormArgs a{static_cast<const uint16_t*>(x), ld_x,
+                            static_cast<const uint16_t*>(residual), ld_res,
+                            static_cast<uint16_t*>(residual_out), ld_res_out,
+                            static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(out),
+                            ld_out, static_cast<uint8_t*>(out_q), ld_q, out_scale, tok, H, eps,
+                            weight_offset, 0};
+  auto rows16 = [](const void* p, int64_t ld) { return !p || (aligned_to(p, 16) && ld % 8 == 0); };
+  const bool al = H % 8 == 0 && rows16(x, ld_x) && rows16(residual, ld_res) &&
+                  rows16(residual_out, ld_res_out) && rows16(weight, 0) && rows16(out, ld_out) &&
+                  (!out_q || (aligned_to(out_q, 8) && ld_q % 8 == 0));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == LORA_BF16)
+    return al ? rmsnorm<lora::Bf16, true>(a, st) : rmsnorm<lora::Bf16, false>(a, st);
+  return al ? rmsnorm<lora::Fp16, true>(a, st) : rmsnorm<lora::Fp16, false>(a, st);
+}
+
+// ------------------------------------------------------------------ rotate and append
+
+extern "C" lora_status lora_rope_append(
+    const void* qkv, int64_t ld_qkv, const int32_t* qkv_offsets, int head_dim, int rotary_dim,
+    const void* positions, int64_t ld_pos, int axes, const uint8_t* axis_map,
+    const float* cos_sin, int64_t max_pos, int interleaved, const void* q_weight,
+    const void* k_weight, float weight_offset, float eps, void* q_out, int64_t ld_q,
+    void* k_cache, const int64_t* k_strides, void* v_cache, const int64_t* v_strides,
+    int64_t num_pages, int page_size, lora_dtype cache_dtype, float k_scale, float v_scale,
+    const void* slots, int index_bytes, int tok, lora_dtype dtype, void* stream) {
+  if (dtype != LORA_BF16 && dtype != LORA_FP16) return LORA_ERR_UNSUPPORTED;
+  if (cache_dtype != dtype && cache_dtype != LORA_E4M3) return LORA_ERR_UNSUPPORTED;
+  if (index_bytes != 4 && index_bytes != 8) return LORA_ERR_UNSUPPORTED;
+  if (!qkv_offsets || !k_strides || !v_strides) return LORA_ERR_INVALID_ARGUMENT;
+  if (tok < 0 || head_dim < 1 || rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 2 ||
+      axes < 1 || num_pages < 0 || page_size < 1 || !(eps >= 0.f))
+    return LORA_ERR_INVALID_ARGUMENT;
+  if (head_dim > lora::kRopeMaxDim || axes > lora::kRopeMaxAxes) return LORA_ERR_UNSUPPORTED;
+  const int32_t* off = qkv_offsets;
+  if (off[0] < 0 || off[1] < off[0] || off[2] < off[1] || off[3] < off[2] || off[3] > ld_qkv)
+    return LORA_ERR_INVALID_ARGUMENT;
+  const int wq = off[1] - off[0], wk = off[2] - off[1], wv = off[3] - off[2];
+  if (wq % head_dim || wk % head_dim || wk != wv || ld_q < wq) return LORA_ERR_INVALID_ARGUMENT;
+  if ((q_weight != nullptr) != (k_weight != nullptr)) return LORA_ERR_INVALID_ARGUMENT;
+  if (!(k_scale > 0.f) || !(v_scale > 0.f)) return LORA_ERR_INVALID_ARGUMENT;
+  if (rotary_dim && (max_pos < 1 || (axes > 1 && (!axis_map || ld_pos < tok))))
+    return LORA_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 3; ++i)
+    if (k_strides[i] < 0 || v_strides[i] < 0) return LORA_ERR_INVALID_ARGUMENT;
+  lora::RopeAppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (axes > 1)
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+      if (axis_map[i] >= axes) return LORA_ERR_INVALID_ARGUMENT;
+      a.axis_of[i >> 3] |= static_cast<uint16_t>(axis_map[i] << (2 * (i & 7)));
+    }
+  if (tok == 0 || wq + wk == 0) return LORA_OK;
+  if (!qkv || !slots || (wq && !q_out) || (wk && num_pages && (!k_cache || !v_cache)) ||
+      (rotary_dim && (!positions || !cos_sin)))
+    return LORA_ERR_INVALID_ARGUMENT;
+  const uintptr_t ib = static_cast<uintptr_t>(index_bytes);
+  const uintptr_t cb = cache_dtype == LORA_E4M3 ? 1 : 2;
+  if (!aligned_to(qkv, 2) || !aligned_to(q_out, 2) || !aligned_to(k_cache, cb) ||
+      !aligned_to(v_cache, cb) || !aligned_to(slots, ib) || !aligned_to(positions, ib) ||
+      !aligned_to(cos_sin, 4) || !aligned_to(q_weight, 2) || !aligned_to(k_weight, 2))
+    return LORA_ERR_INVALID_ARGUMENT;
+  a.qkv = static_cast<const uint16_t*>(qkv);
+  a.ld_qkv = ld_qkv;
+  a.off_q = off[0];
+  a.off_k = off[1];
+  a.off_v = off[2];
+  a.hq = wq / head_dim;
+  a.hkv = wk / head_dim;
+  a.D = head_dim;
+  a.R = rotary_dim;
+  a.positions = positions;
+  a.ld_pos = ld_pos;
+  a.axes = axes;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.ld_q = ld_q;
+  a.kc = k_cache;
+  a.vc = v_cache;
+  a.k_page = k_strides[0];
+  a.k_slot = k_strides[1];
+  a.k_head = k_strides[2];
+  a.v_page = v_strides[0];
+  a.v_slot = v_strides[1];
+  a.v_head = v_strides[2];
+  a.pages = num_pages;
+  a.page_size = page_size;
+  a.slots = slots;
+  a.qw = static_cast<const uint16_t*>(q_weight);
+  a.kw = static_cast<const uint16_t*>(k_weight);
+  a.eps = eps;
+  a.w0 = weight_offset;
+  a.k_inv = 1.f / k_scale;
+  a.v_inv = 1.f / v_scale;
+  a.tok = tok;
+  a.interleaved = interleaved;
+  a.idx64 = index_bytes == 8;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t warps = static_cast<int64_t>(tok) * (a.hq + 2 * a.hkv);
+  if ((warps + 7) / 8 >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
+  const bool c8 = cache_dtype == LORA_E4M3;
+  if (dtype == LORA_BF16) {
+    if (c8) lora::rope_append_general_kernel<lora::Bf16, true><<<grid, 256, 0, st>>>(a);
+    else lora::rope_append_general_kernel<lora::Bf16, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (c8) lora::rope_append_general_kernel<lora::Fp16, true><<<grid, 256, 0, st>>>(a);
+    else lora::rope_append_general_kernel<lora::Fp16, false><<<grid, 256, 0, st>>>(a);
+  }
+  ++g_launches;
+  g_last_path = LORA_PATH_GENERAL;
+  return launch_status();
+}
+
+// ------------------------------------------------------------------ 4-bit base projection
+
+extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,
+                                       const void* W, int64_t ld_w, const void* w_scales,
+                                       const uint8_t* w_zeros, int64_t ld_s, void* out,
+                                       int64_t ld_out, int tok, int K, int N, int group,
+                                       lora_dtype x_dtype, lora_dtype dtype, void* stream) {
+  if (dtype != LORA_BF16 && dtype != LORA_FP16) return LORA_ERR_UNSUPPORTED;
+  if (x_dtype != dtype && x_dtype != LORA_E4M3) return LORA_ERR_UNSUPPORTED;
+  if (group != 32 && group != 64 && group != 128) return LORA_ERR_UNSUPPORTED;
+  if (tok < 0 || K < 1 || N < 0 || ld_x < K || ld_out < N || ld_s < N ||
+      ld_w < static_cast<int64_t>(K + 31) / 32 * 16)
+    return LORA_ERR_INVALID_ARGUMENT;
+  if ((x_scale != nullptr) != (x_dtype == LORA_E4M3)) return LORA_ERR_INVALID_ARGUMENT;
+  if (tok == 0 || N == 0) return LORA_OK;
+  if (!x || !W || !w_scales || !out) return LORA_ERR_INVALID_ARGUMENT;
+  if ((x_dtype != LORA_E4M3 && !aligned_to(x, 2)) || !aligned_to(x_scale, 4) ||
+      !aligned_to(w_scales, 2) || !aligned_to(out, 2))
+    return LORA_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(W, 16) || ld_w % 16) return LORA_ERR_UNSUPPORTED;
+  const lora::W4Args a{x, ld_x, x_scale, static_cast<const uint8_t*>(W), ld_w,
+                       static_cast<const uint16_t*>(w_scales), w_zeros, ld_s,
+                       static_cast<uint16_t*>(out), ld_out, tok, K, N,
+                       group == 32 ? 5 : group == 64 ? 6 : 7};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid(static_cast<unsigned>((N + 7) / 8), static_cast<unsigned>((tok + 3) / 4));
+  const bool x8 = x_dtype == LORA_E4M3;
+  if (dtype == LORA_BF16) {
+    if (x8) lora::w4_simple_kernel<lora::Bf16, true><<<grid, 256, 0, st>>>(a);
+    else lora::w4_simple_kernel<lora::Bf16, false><<<grid, 256, 0, st>>>(a);
+  } else {
+    if (x8) lora::w4_simple_kernel<lora::Fp16, true><<<grid, 256, 0, st>>>(a);
+    else lora::w4_simple_kernel<lora::Fp16, false><<<grid, 256, 0, st>>>(a);
+  }
+  ++g_launches;
+  g_last_path = LORA_PATH_GENERAL;
+  return launch_status();
+}

@@ -1397,3 +1397,5 @@ extern "C" lora_status lora_base_expand(
   return dtype == LORA_BF16 ? base_expand_tc<lora::Bf16>(a, W, ld_w, B_stack, dtype, st)
                             : base_expand_tc<lora::Fp16>(a, W, ld_w, B_stack, dtype, st);
 }
+
+#include "layer_ops.cuh"

@@ -25,6 +25,7 @@ BAD_INDPTR, BAD_ADAPTER, BAD_PERMUTATION, BAD_SLICES = 2, 4, 8, 16
 MAX_SLICES = 8
 
 _P, _I, _L, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_F = ctypes.c_float
 _lib = None
 _lock = threading.Lock()
 
@@ -77,6 +78,15 @@ def lib() -> ctypes.CDLL:
             l.lora_base_expand.argtypes = [_P, _L, _P, _L, _P, _L, _P, _P, _P, _P, _P, _P, _P,
                                            _L] + [_I] * 8 + [_P]
             l.lora_base_expand.restype = _I
+            l.lora_rmsnorm.argtypes = [_P, _L, _P, _L, _P, _L, _P, _F, _F, _P, _L, _P, _L, _P] + \
+                [_I] * 3 + [_P]
+            l.lora_rmsnorm.restype = _I
+            l.lora_w4_project.argtypes = [_P, _L, _P, _P, _L, _P, _P, _L, _P, _L] + [_I] * 6 + [_P]
+            l.lora_w4_project.restype = _I
+            l.lora_rope_append.argtypes = [_P, _L, _P, _I, _I, _P, _L, _I, _P, _P, _L, _I, _P, _P,
+                                           _F, _F, _P, _L, _P, _P, _P, _P, _L, _I, _I, _F, _F, _P,
+                                           _I, _I, _I, _P]
+            l.lora_rope_append.restype = _I
             _lib = l
     return _lib
 
@@ -402,6 +412,328 @@ def lora_base_expand(x: torch.Tensor, W: torch.Tensor, in_r: torch.Tensor,
     if st != LORA_OK:
         raise LoraError("lora_base_expand", st)
     return out
+
+
+# ----------------------------------------------------------------------------
+# operators around the adapted projection
+# ----------------------------------------------------------------------------
+
+_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, tok: int, width: int, device) -> int:
+    """Checks a [tok, >= width] tensor of unit inner stride; returns its row stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 2 or t.shape[0] != tok or t.shape[1] < width:
+        raise ValueError(f"{name} must be [{tok}, >= {width}], got {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and width > 1:
+        raise ValueError(f"{name} must have a unit inner stride")
+    if tok <= 1:  # the only row's stride says nothing
+        return max(ld, width)
+    if ld < width:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return ld
+
+
+def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> int:
+    """Checks a contiguous 1-D tensor of n elements; returns its address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor on {device}")
+    return t.data_ptr()
+
+
+def _call_on(device: torch.device, name: str, fn, args, stream) -> None:
+    """Calls an entry point with the tensors' device current, on the given
+    stream or that device's current one."""
+    if device.type != "cuda":
+        raise ValueError(f"{name} needs CUDA tensors, got {device}")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = _stream(stream)
+    if device.index == torch._C._cuda_getDevice():
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    if st != LORA_OK:
+        raise LoraError(name, st)
+
+
+def lora_rmsnorm(x: torch.Tensor, weight: torch.Tensor, out: Optional[torch.Tensor], *,
+                 residual: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 weight_offset: float = 0.0, out_q: Optional[torch.Tensor] = None,
+                 out_scale: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of h = x + residual: out = h * rsqrt(mean(h^2) + eps) * (weight + weight_offset).
+
+    x, residual, out [tok, H] (unit inner stride) and weight [H] share bf16 or
+    fp16; h is rounded and written to residual_out (default: residual, in
+    place).  out_q [tok, H] (float8_e4m3fn) with out_scale [tok] (fp32) takes
+    the 8-bit form, out = out_q * out_scale[:, None] within rounding; `out` may
+    then be None.  Returns out, or out_q where out is None."""
+    dt = _dtype_code(x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
+    tok, H = x.shape
+    dtype, dev = x.dtype, x.device
+    ld_x = _rows(x, "x", dtype, tok, H, dev)
+    w = _flat(weight, "weight", dtype, H, dev)
+    ptr_r = ptr_ro = ptr_o = ptr_q = ptr_s = None
+    ld_r = ld_ro = ld_o = ld_q = 0
+    if residual is not None:
+        ld_r, ptr_r = _rows(residual, "residual", dtype, tok, H, dev), residual.data_ptr()
+        ld_ro, ptr_ro = ld_r, ptr_r
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        ld_ro = _rows(residual_out, "residual_out", dtype, tok, H, dev)
+        ptr_ro = residual_out.data_ptr()
+    if out is not None:
+        ld_o, ptr_o = _rows(out, "out", dtype, tok, H, dev), out.data_ptr()
+    if (out_q is None) != (out_scale is None):
+        raise ValueError("out_q and out_scale go together")
+    if out_q is not None:
+        ld_q = _rows(out_q, "out_q", torch.float8_e4m3fn, tok, H, dev)
+        ptr_q = out_q.data_ptr()
+        ptr_s = _flat(out_scale, "out_scale", torch.float32, tok, dev)
+    elif out is None:
+        raise ValueError("out or out_q is required")
+    if tok:
+        _call_on(dev, "lora_rmsnorm", lib().lora_rmsnorm,
+                 (x.data_ptr(), ld_x, ptr_r, ld_r, ptr_ro, ld_ro, w, weight_offset, eps, ptr_o,
+                  ld_o, ptr_q, ld_q, ptr_s, tok, H, dt), stream)
+    return out if out is not None else out_q
+
+
+def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor,
+                    out: torch.Tensor, *, group_size: int,
+                    w_zeros: Optional[torch.Tensor] = None,
+                    x_scale: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Base projection with 4-bit weights: out = x @ W^T with
+    W[n, k] = w_scales[k // group_size, n] * (q[n, k] - w_zeros[k // group_size, n]).
+
+    x [tok, K] (unit inner stride) of out's element type, or float8_e4m3fn
+    with x_scale [tok] (fp32); w_packed [N, >= ceil(K/32)*16] uint8 holds q as
+    :func:`w4_pack` lays it out; w_scales [ceil(K/group_size), N] of out's
+    type; w_zeros uint8 of the same shape (default: 8 everywhere); out [tok,
+    >= N] is written in its first N columns."""
+    dt = _dtype_code(out)
+    if x.dim() != 2 or w_packed.dim() != 2:
+        raise ValueError("x and w_packed must be 2-D")
+    tok, K = x.shape
+    N = w_packed.shape[0]
+    dev = x.device
+    x_dt = _CODES.get(x.dtype, -1)
+    if x_dt != 2 and x_dt != dt:
+        raise TypeError(f"x must be {out.dtype} or float8_e4m3fn, got {x.dtype}")
+    if group_size not in (32, 64, 128):
+        raise ValueError("group_size must be 32, 64 or 128")
+    if K < 1:
+        raise ValueError("x must have at least one column")
+    G = -(-K // group_size)
+    ld_x = _rows(x, "x", x.dtype, tok, K, dev)
+    ld_w = _rows(w_packed, "w_packed", torch.uint8, N, -(-K // 32) * 16, dev)
+    if N == 1:  # a single row of any stride, packed in whole 16-byte blocks
+        ld_w = -(-K // 32) * 16
+    ld_s = _rows(w_scales, "w_scales", out.dtype, G, N, dev)
+    if w_scales.shape[1] != N:
+        raise ValueError(f"w_scales must be [{G}, {N}], got {tuple(w_scales.shape)}")
+    ptr_z = ptr_sx = None
+    if w_zeros is not None:
+        if _rows(w_zeros, "w_zeros", torch.uint8, G, N, dev) != ld_s or w_zeros.shape[1] != N:
+            raise ValueError("w_zeros must have the shape and row stride of w_scales")
+        ptr_z = w_zeros.data_ptr()
+    if (x_scale is not None) != (x_dt == 2):
+        raise ValueError("x_scale goes with an 8-bit x")
+    if x_scale is not None:
+        ptr_sx = _flat(x_scale, "x_scale", torch.float32, tok, dev)
+    ld_o = _rows(out, "out", out.dtype, tok, N, dev)
+    if tok and N:
+        _call_on(dev, "lora_w4_project", lib().lora_w4_project,
+                 (x.data_ptr(), ld_x, ptr_sx, w_packed.data_ptr(), ld_w, w_scales.data_ptr(),
+                  ptr_z, ld_s, out.data_ptr(), ld_o, tok, K, N, group_size, x_dt, dt), stream)
+    return out
+
+
+# the place of value i of eight in a 32-bit word of packed weights
+_W4_SHIFT = (0, 16, 4, 20, 8, 24, 12, 28)
+
+
+def w4_pack(q: torch.Tensor) -> torch.Tensor:
+    """Packs integers q [N, K] in 0..15 as lora_w4_project reads them: uint8
+    [N, ceil(K/32)*16], the values behind K being 0."""
+    if q.dim() != 2 or q.dtype.is_floating_point or q.dtype.is_complex or q.dtype == torch.bool:
+        raise ValueError("q must be a 2-D integer tensor")
+    if q.numel() and (int(q.min()) < 0 or int(q.max()) > 15):
+        raise ValueError("4-bit values must be in 0..15")
+    N, K = q.shape
+    words = torch.zeros(N, -(-K // 32) * 32, dtype=torch.int64, device=q.device)
+    words[:, :K] = q
+    shift = torch.tensor(_W4_SHIFT, dtype=torch.int64, device=q.device)
+    words = (words.view(N, -1, 8) << shift).sum(dim=2)
+    bytes_ = (words[:, :, None] >> torch.arange(0, 32, 8, device=q.device)) & 255
+    return bytes_.to(torch.uint8).reshape(N, -1)
+
+
+def w4_unpack(w_packed: torch.Tensor, K: int) -> torch.Tensor:
+    """The integers [N, K] (uint8) of weights packed by :func:`w4_pack`."""
+    if w_packed.dim() != 2 or w_packed.dtype != torch.uint8 or w_packed.shape[1] % 4:
+        raise ValueError("w_packed must be a 2-D uint8 tensor of whole 32-bit words a row")
+    if not 0 <= K <= 2 * w_packed.shape[1]:
+        raise ValueError(f"rows of {w_packed.shape[1]} bytes do not hold {K} values")
+    b = w_packed.reshape(w_packed.shape[0], -1, 4)
+    q = torch.stack([(b[:, :, s // 8] >> (s % 8)) & 15 for s in _W4_SHIFT], dim=2)
+    return q.reshape(w_packed.shape[0], -1)[:, :K].contiguous()
+
+
+def w4_quantize(W: torch.Tensor, group_size: int = 128, zeros: bool = False):
+    """Rounds a weight W [N, K] (bf16 or fp16) to 4 bits in groups of
+    group_size columns: returns (w_packed, w_scales [G, N], w_zeros [G, N] or
+    None).  With `zeros` a group spans its smallest to its largest value (and
+    0), without it q - 8 spans plus and minus its largest magnitude."""
+    dt = W.dtype
+    _dtype_code(W)
+    if W.dim() != 2 or group_size not in (32, 64, 128):
+        raise ValueError("W must be 2-D and group_size 32, 64 or 128")
+    N, K = W.shape
+    G = -(-K // group_size)
+    Wf = torch.zeros(N, G * group_size, dtype=torch.float32, device=W.device)
+    Wf[:, :K] = W
+    Wg = Wf.view(N, G, group_size)
+    if zeros:
+        lo, hi = Wg.amin(2).clamp(max=0), Wg.amax(2).clamp(min=0)
+        s = (hi - lo) / 15
+    else:
+        s = Wg.abs().amax(2) / 7
+    s = s.to(dt)
+    # the scale that is stored is the one that values are divided by
+    sf = torch.where(s > 0, s.float(), 1.0)
+    z = (-lo / sf).round().clamp(0, 15) if zeros else torch.full_like(sf, 8.0)
+    q = ((Wg / sf[:, :, None]).round() + z[:, :, None]).clamp(0, 15).to(torch.uint8)
+    return (w4_pack(q.reshape(N, -1)[:, :K]), s.T.contiguous(),
+            z.to(torch.uint8).T.contiguous() if zeros else None)
+
+
+def rope_axis_map(sections: Sequence[int], interleaved: bool = False) -> list:
+    """The position axis of each frequency for :func:`lora_rope_append`.
+
+    sections: frequencies of each axis (time, height, width, ...).  In order,
+    an axis' frequencies are neighbours; interleaved, frequency i belongs to
+    axis i % len(sections) as long as that axis has frequencies left, counted
+    as i < len(sections) * sections[axis], and to axis 0 otherwise."""
+    sec = [int(v) for v in sections]
+    if not 1 <= len(sec) <= 4 or min(sec) < 0:
+        raise ValueError("need 1 to 4 non-negative sections")
+    if not interleaved:
+        return [a for a, n in enumerate(sec) for _ in range(n)]
+    m = len(sec)
+    return [i % m if i < m * sec[i % m] else 0 for i in range(sum(sec))]
+
+
+def _cache(t: torch.Tensor, name: str, hkv: int, D: int, device):
+    """Checks a [pages, page_size, Hkv, D] cache of any strides but the last."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 4 or t.shape[2] != hkv or t.shape[3] != D:
+        raise ValueError(f"{name} must be [pages, page_size, {hkv}, {D}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1 and D > 1:
+        raise ValueError(f"{name} must have a unit inner stride")
+    return (ctypes.c_int64 * 3)(st[0], st[1], st[2])
+
+
+def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: int,
+                     positions: torch.Tensor, cos_sin: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, slots: torch.Tensor, *,
+                     q_out: Optional[torch.Tensor] = None,
+                     axis_map: Optional[Sequence[int]] = None, interleaved: bool = False,
+                     q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     weight_offset: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0,
+                     stream=None) -> torch.Tensor:
+    """Rotates the q and k slices of qkv, writes q to q_out and appends k and v
+    to a paged cache.
+
+    qkv [tok, >= off[3]] with the q, k, v slices at the host offsets
+    slice_offsets[0..3], heads of head_dim columns; positions [tok], or
+    [axes, tok] with axis_map (one axis number for each frequency, see
+    :func:`rope_axis_map`); cos_sin [max_pos, R] fp32, R/2 cosines and R/2
+    sines, R <= head_dim even; k_cache, v_cache [pages, page_size, Hkv,
+    head_dim] of qkv's type or float8_e4m3fn (values divided by k_scale,
+    v_scale), any strides but a unit inner one; slots [tok], negative = no
+    cache entry.  positions and slots are both int32 or both int64.  q_weight
+    and k_weight [head_dim] normalise each head first.  q_out [tok, Hq *
+    head_dim] defaults to the q slice itself, in place."""
+    dt = _dtype_code(qkv)
+    if qkv.dim() != 2:
+        raise ValueError(f"qkv must be 2-D, got {tuple(qkv.shape)}")
+    if len(slice_offsets) != 4:
+        raise ValueError("slice_offsets needs 4 entries")
+    o0, o1, o2, o3 = slice_offsets
+    tok, dev, D = qkv.shape[0], qkv.device, head_dim
+    if not 0 <= o0 <= o1 <= o2 <= o3 or D < 1 or (o1 - o0) % D or (o2 - o1) % D or \
+            o3 - o2 != o2 - o1:
+        raise ValueError("slice_offsets must span whole heads, as many of k as of v")
+    ld = _rows(qkv, "qkv", qkv.dtype, tok, o3, dev)
+    idt = slots.dtype
+    if idt not in (torch.int32, torch.int64) or positions.dtype != idt:
+        raise TypeError("positions and slots must both be int32 or both int64")
+    ptr_s = _flat(slots, "slots", idt, tok, dev)
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or \
+            cos_sin.device != dev:
+        raise ValueError(f"cos_sin must be a contiguous fp32 [max_pos, R] tensor on {dev}")
+    max_pos, R = cos_sin.shape
+    if R > D or R % 2 or (R and max_pos < 1):
+        raise ValueError("cos_sin must have 2 * frequencies <= head_dim columns and a row")
+    if positions.dim() == 1:
+        axes, ld_pos = 1, 0
+        _flat(positions, "positions", idt, tok, dev)
+        if axis_map is not None:
+            raise ValueError("axis_map needs positions of [axes, tok]")
+        amap = None
+    else:
+        axes = positions.shape[0]
+        ld_pos = _rows(positions, "positions", idt, axes, tok, dev)
+        if positions.shape[1] != tok or not 1 <= axes <= 4:
+            raise ValueError(f"positions must be [tok] or [1..4, {tok}]")
+        if axis_map is None and axes > 1:
+            raise ValueError("positions of several axes need an axis_map")
+        amap = bytes(axis_map) if axis_map is not None else None
+        if amap is not None and (len(amap) != R // 2 or (amap and max(amap) >= axes)):
+            raise ValueError(f"axis_map needs {R // 2} axis numbers below {axes}")
+    hkv = (o2 - o1) // D
+    ks = _cache(k_cache, "k_cache", hkv, D, dev)
+    vs = _cache(v_cache, "v_cache", hkv, D, dev)
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must share shape and element type")
+    c_dt = _CODES.get(k_cache.dtype, -1)
+    if c_dt != dt and c_dt != 2:
+        raise TypeError(f"the caches must be {qkv.dtype} or float8_e4m3fn, got {k_cache.dtype}")
+    if q_out is None:
+        q_out = qkv[:, o0:o1]
+    ld_q = _rows(q_out, "q_out", qkv.dtype, tok, o1 - o0, dev)
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    qw = kw = None
+    if q_weight is not None:
+        qw = _flat(q_weight, "q_weight", qkv.dtype, D, dev)
+        kw = _flat(k_weight, "k_weight", qkv.dtype, D, dev)
+    if tok:
+        _call_on(dev, "lora_rope_append", lib().lora_rope_append,
+                 (qkv.data_ptr(), ld, (ctypes.c_int32 * 4)(o0, o1, o2, o3), D, R,
+                  positions.data_ptr(), ld_pos, axes, amap, cos_sin.data_ptr(), max_pos,
+                  int(interleaved), qw, kw, weight_offset, eps, q_out.data_ptr(), ld_q,
+                  k_cache.data_ptr(), ks, v_cache.data_ptr(), vs,
+                  k_cache.shape[0] if k_cache.shape[1] else 0, max(k_cache.shape[1], 1), c_dt, k_scale, v_scale, ptr_s, idt.itemsize, tok, dt),
+                 stream)
+    return q_out
 
 
 def lora_validate(seg_indptr: torch.Tensor, weight_indices: torch.Tensor,
