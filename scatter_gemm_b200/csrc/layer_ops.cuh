@@ -6,6 +6,32 @@
 #include "rmsnorm.cuh"
 #include "rope_append.cuh"
 #include "w4.cuh"
+#include "w4_tc.cuh"
+
+#include <algorithm>
+#include <type_traits>
+
+#ifndef LORA_W4_MV_TOKENS
+#define LORA_W4_MV_TOKENS 8  // 4-bit projection: tokens up to which w4_mv runs
+#endif
+
+namespace {
+
+// Lets a kernel take up to `bytes` of dynamic shared memory, once for each
+// device (`ready` holds a bit for each).
+bool set_smem_once(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  const uint64_t bit = uint64_t(1) << dev;
+  if (ready.load(std::memory_order_acquire) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  ready.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
+}  // namespace
 
 // ------------------------------------------------------------------ RMS norm
 
@@ -177,6 +203,116 @@ extern "C" lora_status lora_rope_append(
 
 // ------------------------------------------------------------------ 4-bit base projection
 
+namespace {
+
+// 2-D map of bytes or 16-bit elements, box {box_cols, box_rows}.
+bool encode_w4(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t cols,
+               uint64_t rows, uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows,
+               CUtensorMapSwizzle swz) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kW4Smem = 225 * 1024;
+constexpr int kMvSmem = 200 * 1024;
+
+template <class E, bool X8, int NT, int VW>
+lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
+  const int rows = std::min(a.tok, 8 * NT);
+  const int red = 2 * lora::kMvWarps * NT * 128 * 4;
+  int kc = round_up(a.K, 128);
+  auto bytes = [&](int k) { return rows * lora::mv_row_bytes(k) + red; };
+  if (bytes(kc) > kMvSmem) kc = ((kMvSmem - red) / rows - 64) / 256 * 128;
+  const int smem = bytes(kc);
+  const int occ = std::max(1, std::min(2, 220 * 1024 / (smem + 1024)));
+  const int tiles = (a.N + 15) / 16;
+  const dim3 grid(std::min(tiles, sms * occ), (a.tok + 8 * NT - 1) / (8 * NT));
+  auto kernel = lora::w4_mv_kernel<E, X8, NT, VW>;
+  static std::atomic<uint64_t> ready{0};  // a bit for each device
+  if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kMvSmem)) return LORA_ERR_CUDA;
+  kernel<<<grid, lora::kMvThreads, smem, st>>>(a, kc);
+  ++g_launches;
+  g_last_path = LORA_PATH_GENERAL;
+  return launch_status();
+}
+
+template <class E, bool X8, int NT, int GS, int NW>
+lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
+  using C = lora::W4Tc<E, X8, NT, GS, NW>;
+  lora::W4TcParams P;
+  std::memset(&P, 0, sizeof(P));
+  P.a = a;
+  P.tiles_n = (a.N + lora::kW4M - 1) / lora::kW4M;
+  P.tiles_t = (a.tok + NT - 1) / NT;
+  P.nkb = (a.K + lora::kW4K - 1) / lora::kW4K;
+  const int64_t tiles = static_cast<int64_t>(P.tiles_n) * P.tiles_t;
+  if (tiles > (1 << 28)) return LORA_ERR_UNSUPPORTED;
+  constexpr int kPerSm = C::kMinBlocks;
+  const int slots = sms * kPerSm;
+  P.cs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(8, P.nkb), slots / tiles)));
+  // 256 TMEM columns: at most two such blocks to an SM (kTmemCtaMinSmem); 512:
+  // no other block with TMEM fits beside it
+  const int cap = kPerSm == 2 ? 110 * 1024 : 220 * 1024;
+  const int fixed = 1024 + 256 + 8 * 64;
+  P.stages = std::min(16, (cap - fixed) / C::kStage);
+  const size_t smem = std::max<size_t>(P.stages * C::kStage + fixed,
+                                       kPerSm == 2 ? kTmemCtaMinSmem : 2 * kTmemCtaMinSmem);
+  P.idesc = lora::make_idesc_f16(!X8 && std::is_same<E, lora::Bf16>::value ? 1 : 0, lora::kW4M, NT);
+  const CUtensorMapDataType xt = X8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : std::is_same<E, lora::Bf16>::value
+                                     ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!encode_w4(&P.tmap_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, (a.K + 31) / 32 * 16, a.N, a.ld_w,
+                 64, lora::kW4M, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !encode_w4(&P.tmap_x, xt, a.x, a.K, a.tok, a.ld_x * (X8 ? 1 : 2), X8 ? 128 : 64, NT,
+                 CU_TENSOR_MAP_SWIZZLE_128B))
+    return LORA_ERR_CUDA;
+  auto kernel = lora::w4_tc_kernel<E, X8, NT, GS, NW>;
+  static std::atomic<uint64_t> ready{0};  // a bit for each device
+  if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem)) return LORA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(P.cs > 1 ? tiles * P.cs : std::min<int64_t>(tiles, slots)));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  LaunchAttrs la;
+  if (P.cs > 1) la.cluster(static_cast<unsigned>(P.cs));
+  la.apply(cfg);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+  ++g_launches;
+  g_last_path = LORA_PATH_TENSOR | (P.cs > 1 ? LORA_PATH_SPLITK : 0);
+  return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
+template <class E, bool X8, int GS>
+lora_status w4_project_group(const lora::W4Args& a, int sms, cudaStream_t st) {
+  constexpr int VW = 1 << (GS - 5);
+  const int64_t ldb = a.ld_x * (X8 ? 1 : 2);
+  const bool tma_x = aligned_to(a.x, 16) && ldb % 16 == 0;
+  if (a.tok <= LORA_W4_MV_TOKENS || !tma_x)
+    return a.tok <= 8 ? w4_mv<E, X8, 1, VW>(a, sms, st) : w4_mv<E, X8, 2, VW>(a, sms, st);
+  if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4>(a, sms, st);
+  if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4>(a, sms, st);
+  if (a.tok <= 64) return w4_tc<E, X8, 64, GS, 4>(a, sms, st);
+  return w4_tc<E, X8, 128, GS, 8>(a, sms, st);
+}
+
+template <class E, bool X8>
+lora_status w4_project(const lora::W4Args& a, int sms, cudaStream_t st) {
+  if (a.group_shift == 5) return w4_project_group<E, X8, 5>(a, sms, st);
+  if (a.group_shift == 6) return w4_project_group<E, X8, 6>(a, sms, st);
+  return w4_project_group<E, X8, 7>(a, sms, st);
+}
+
+}  // namespace
+
 extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,
                                        const void* W, int64_t ld_w, const void* w_scales,
                                        const uint8_t* w_zeros, int64_t ld_s, void* out,
@@ -199,17 +335,13 @@ extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float*
                        static_cast<const uint16_t*>(w_scales), w_zeros, ld_s,
                        static_cast<uint16_t*>(out), ld_out, tok, K, N,
                        group == 32 ? 5 : group == 64 ? 6 : 7};
+  const DeviceFacts* dev = device_facts();
+  if (!dev) return LORA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>((N + 7) / 8), static_cast<unsigned>((tok + 3) / 4));
   const bool x8 = x_dtype == LORA_E4M3;
-  if (dtype == LORA_BF16) {
-    if (x8) lora::w4_simple_kernel<lora::Bf16, true><<<grid, 256, 0, st>>>(a);
-    else lora::w4_simple_kernel<lora::Bf16, false><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (x8) lora::w4_simple_kernel<lora::Fp16, true><<<grid, 256, 0, st>>>(a);
-    else lora::w4_simple_kernel<lora::Fp16, false><<<grid, 256, 0, st>>>(a);
-  }
-  ++g_launches;
-  g_last_path = LORA_PATH_GENERAL;
-  return launch_status();
+  if (dtype == LORA_BF16)
+    return x8 ? w4_project<lora::Bf16, true>(a, dev->sms, st)
+              : w4_project<lora::Bf16, false>(a, dev->sms, st);
+  return x8 ? w4_project<lora::Fp16, true>(a, dev->sms, st)
+            : w4_project<lora::Fp16, false>(a, dev->sms, st);
 }
