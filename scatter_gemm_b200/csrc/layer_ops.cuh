@@ -12,7 +12,7 @@
 #include <type_traits>
 
 #ifndef LORA_W4_MV_TOKENS
-#define LORA_W4_MV_TOKENS 8  // 4-bit projection: tokens up to which w4_mv runs
+#define LORA_W4_MV_TOKENS 16 // 4-bit projection: tokens up to which w4_mv runs
 #endif
 
 namespace {
@@ -223,29 +223,38 @@ bool encode_w4(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint6
 constexpr int kW4Smem = 225 * 1024;
 constexpr int kMvSmem = 200 * 1024;
 
-template <class E, bool X8, int NT, int VW>
+template <class E, bool X8, int NT, int VW, int WARPS>
 lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
-  const int rows = std::min(a.tok, 8 * NT);
-  const int red = 2 * lora::kMvWarps * NT * 128 * 4;
-  int kc = round_up(a.K, 128);
-  auto bytes = [&](int k) { return rows * lora::mv_row_bytes(k) + red; };
-  if (bytes(kc) > kMvSmem) kc = ((kMvSmem - red) / rows - 64) / 256 * 128;
-  const int smem = bytes(kc);
-  const int occ = std::max(1, std::min(2, 220 * 1024 / (smem + 1024)));
+  const int64_t blocks = (a.K + 127) / 128;
   const int tiles = (a.N + 15) / 16;
-  const dim3 grid(std::min(tiles, sms * occ), (a.tok + 8 * NT - 1) / (8 * NT));
-  auto kernel = lora::w4_mv_kernel<E, X8, NT, VW>;
+  const int per_sm = WARPS == 8 ? LORA_MV_OCC : 1;
+  // staged x and sums of x for tt tokens, parts of the tiles for n blocks an SM
+  int tt = std::min(a.tok, 8 * NT);
+  auto run = [&](int n) { return std::min((tiles + sms * n - 1) / (sms * n), lora::kMvTiles); };
+  auto bytes = [&](int n) {
+    return tt * static_cast<int64_t>(lora::mv_row_bytes(static_cast<int>(blocks) * 128)) +
+           blocks * (4 / VW) * NT * 32 + (run(n) + WARPS - 1) * NT * 512;
+  };
+  while (tt > 1 && bytes(1) > kMvSmem) --tt;
+  if (bytes(1) > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
+  int occ = per_sm;
+  while (occ > 1 && occ * (bytes(occ) + 1024) > 227 * 1024) --occ;
+  const int smem = static_cast<int>(bytes(occ));
+  const int64_t gy = (a.tok + tt - 1) / tt;
+  if (gy > 65535) return LORA_ERR_UNSUPPORTED;
+  const dim3 grid(std::min(tiles, sms * occ), static_cast<unsigned>(gy));
+  auto kernel = lora::w4_mv_kernel<E, X8, NT, VW, WARPS>;
   static std::atomic<uint64_t> ready{0};  // a bit for each device
   if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kMvSmem)) return LORA_ERR_CUDA;
-  kernel<<<grid, lora::kMvThreads, smem, st>>>(a, kc);
+  kernel<<<grid, 32 * WARPS, smem, st>>>(a, tt);
   ++g_launches;
   g_last_path = LORA_PATH_GENERAL;
   return launch_status();
 }
 
-template <class E, bool X8, int NT, int GS, int NW>
+template <class E, bool X8, int NT, int GS, int SETS, int SW>
 lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
-  using C = lora::W4Tc<E, X8, NT, GS, NW>;
+  using C = lora::W4Tc<X8, NT, GS, SETS, SW>;
   lora::W4TcParams P;
   std::memset(&P, 0, sizeof(P));
   P.a = a;
@@ -254,16 +263,12 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
   P.nkb = (a.K + lora::kW4K - 1) / lora::kW4K;
   const int64_t tiles = static_cast<int64_t>(P.tiles_n) * P.tiles_t;
   if (tiles > (1 << 28)) return LORA_ERR_UNSUPPORTED;
-  constexpr int kPerSm = C::kMinBlocks;
-  const int slots = sms * kPerSm;
-  P.cs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(8, P.nkb), slots / tiles)));
-  // 256 TMEM columns: at most two such blocks to an SM (kTmemCtaMinSmem); 512:
-  // no other block with TMEM fits beside it
-  const int cap = kPerSm == 2 ? 110 * 1024 : 220 * 1024;
+  P.cs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(8, P.nkb), sms / tiles)));
+  // all 512 TMEM columns: with this much shared memory no other block that
+  // takes TMEM fits beside it (they ask for kTmemCtaMinSmem at least)
   const int fixed = 1024 + 256 + 8 * 64;
-  P.stages = std::min(16, (cap - fixed) / C::kStage);
-  const size_t smem = std::max<size_t>(P.stages * C::kStage + fixed,
-                                       kPerSm == 2 ? kTmemCtaMinSmem : 2 * kTmemCtaMinSmem);
+  P.stages = std::min(16, (220 * 1024 - fixed) / C::kStage) / C::kRing * C::kRing;
+  const size_t smem = std::max<size_t>(P.stages * C::kStage + fixed, 2 * kTmemCtaMinSmem);
   P.idesc = lora::make_idesc_f16(!X8 && std::is_same<E, lora::Bf16>::value ? 1 : 0, lora::kW4M, NT);
   const CUtensorMapDataType xt = X8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : std::is_same<E, lora::Bf16>::value
@@ -274,11 +279,11 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
       !encode_w4(&P.tmap_x, xt, a.x, a.K, a.tok, a.ld_x * (X8 ? 1 : 2), X8 ? 128 : 64, NT,
                  CU_TENSOR_MAP_SWIZZLE_128B))
     return LORA_ERR_CUDA;
-  auto kernel = lora::w4_tc_kernel<E, X8, NT, GS, NW>;
+  auto kernel = lora::w4_tc_kernel<E, X8, NT, GS, SETS, SW>;
   static std::atomic<uint64_t> ready{0};  // a bit for each device
   if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem)) return LORA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(P.cs > 1 ? tiles * P.cs : std::min<int64_t>(tiles, slots)));
+  cfg.gridDim = dim3(static_cast<unsigned>(P.cs > 1 ? tiles * P.cs : std::min<int64_t>(tiles, sms)));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -297,11 +302,11 @@ lora_status w4_project_group(const lora::W4Args& a, int sms, cudaStream_t st) {
   const int64_t ldb = a.ld_x * (X8 ? 1 : 2);
   const bool tma_x = aligned_to(a.x, 16) && ldb % 16 == 0;
   if (a.tok <= LORA_W4_MV_TOKENS || !tma_x)
-    return a.tok <= 8 ? w4_mv<E, X8, 1, VW>(a, sms, st) : w4_mv<E, X8, 2, VW>(a, sms, st);
-  if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4>(a, sms, st);
-  if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4>(a, sms, st);
-  if (a.tok <= 64) return w4_tc<E, X8, 64, GS, 4>(a, sms, st);
-  return w4_tc<E, X8, 128, GS, 8>(a, sms, st);
+    return a.tok <= 8 ? w4_mv<E, X8, 1, VW, 8>(a, sms, st) : w4_mv<E, X8, 2, VW, 16>(a, sms, st);
+  if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4, 4>(a, sms, st);
+  if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4, 4>(a, sms, st);
+  if (a.tok <= 64) return w4_tc<E, X8, 64, GS, 4, 8>(a, sms, st);
+  return w4_tc<E, X8, 128, GS, 2, 8>(a, sms, st);
 }
 
 template <class E, bool X8>

@@ -11,6 +11,8 @@
 // exact too; a group's sum is scaled in fp32 before it joins the others.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "rmsnorm.cuh"
 #include "sm100.cuh"
@@ -98,114 +100,165 @@ __device__ __forceinline__ void w4_mma<Fp16>(float (&c)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kMvWarps = 8;
-constexpr int kMvThreads = 32 * kMvWarps;
-constexpr int kMvDepth = 4;  // blocks of 128 K that a warp has in flight
+// What turns packed weights into operands of w4_mv without arithmetic: the bit
+// patterns 0 .. 255 of bf16 and of fp16 are the numbers 0 .. 255 times their
+// smallest subnormal, 2^-133 or 2^-24, so four masked bits are q (or 16 q,
+// where they stand four places up) as they are.  bf16 products are kept in
+// fp32's normal range by taking x times 2^64: values of x from 2^63 on become
+// infinite, and products of |x| under 2^-57 lose bits.
+template <class E> struct MvScale;
+template <> struct MvScale<Bf16> {
+  static constexpr float kX = 0x1p64f, kOut = 0x1p69f;
+};
+template <> struct MvScale<Fp16> {
+  static constexpr float kX = 1.f, kOut = 0x1p24f;
+};
+
+#ifndef LORA_MV_OCC
+#define LORA_MV_OCC 2
+#endif
+#ifndef LORA_MV_DEPTH
+#define LORA_MV_DEPTH 4
+#endif
+constexpr int kMvDepth = LORA_MV_DEPTH;  // blocks of 128 K that a warp has in flight
+constexpr int kMvTiles = 16;             // row tiles of a block between two passes over their parts
 
 // Bytes between the staged rows of x: a multiple of 128 plus 64, so that the
 // two tokens that a quarter of a warp reads lie in different banks.
 __host__ __device__ __forceinline__ int mv_row_bytes(int kc) { return kc * 2 + 64; }
 
-// One block of a warp: 16 rows of 128 weights, its scales and zero points.
-template <int VW>
+// One block of a warp: 16 rows of 128 weights, and the scale and zero point of
+// each of its rows and groups, spread over the lanes of the row: lane t of a
+// row holds group t % groups.  All as loaded: arithmetic on a value that is on
+// its way would wait for it.
 struct MvBlock {
   uint32_t w[2][4];
-  uint16_t s[2][4 / VW];
-  uint8_t z[2][4 / VW];
+  uint32_t s[2], z[2];
 };
 
 // Few tokens: a block of threads keeps up to 8*NT tokens of x in shared memory
 // and goes over tiles of 16 weight rows; its warps share the K range, each
 // reading weights straight into registers, several blocks ahead, and multiply
 // by mma.sync (16 rows x 8 tokens x 16 K): one fragment of weights serves
-// eight tokens without a trip through shared memory.
+// eight tokens without a trip through shared memory.  The weights enter as the
+// unsigned q; with xs, the sum of the group's x,
+//   sum_k x (q - z) = sum_k x q - z xs
+// at the cost of one bit of the fp32 sums, and widening a word takes one shift
+// and four masks.
 //
 // The pairs of a fragment may be any 16 values of k as long as both operands
 // agree.  Lane t of a row takes VW neighbouring words, so that one load is
 // 4*VW bytes and the 16 values of a product lie in one group of 32*VW weights:
 // VW = 4, 2, 1 for groups of 128, 64, 32.
 //
-// grid = (row tiles in turn, token tiles).  kc: values of x staged at a time
-// (all of K wherever they fit).
-template <class E, bool X8, int NT, int VW>
-__global__ void __launch_bounds__(kMvThreads) w4_mv_kernel(const W4Args p, const int kc) {
+// A block owns a run of row tiles, and its warps share the run's blocks of
+// 16 x 128 weights evenly, in order, across tile borders: a warp's parts of its
+// tiles go to shared memory, and one pass at the end adds each tile's parts in
+// that order.
+//
+// grid = (runs of row tiles, token tiles of `tt` tokens).
+template <class E, bool X8, int NT, int VW, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? LORA_MV_OCC : 1)
+w4_mv_kernel(const W4Args p, const int tt) {
+  using C = typename std::conditional<X8, Fp16, E>::type;  // the operands' type
   extern __shared__ __align__(128) uint8_t mv_smem[];
   constexpr int kSub = 4 / VW;  // groups of a block
+  constexpr int kThreads = 32 * WARPS;
+  constexpr int kPart = NT * 128;  // sums of a tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int t0 = blockIdx.y * 8 * NT;
-  const int ntok = min(8 * NT, p.tok - t0);
-  const int rowb = mv_row_bytes(kc);
-  float* red = reinterpret_cast<float*>(mv_smem + ntok * rowb);  // [2][warps][8 NT][16]
+  const int t0 = blockIdx.y * tt;
+  const int ntok = min(tt, p.tok - t0);
+  const int blocks = (p.K + 127) / 128;
+  const int rowb = mv_row_bytes(blocks * 128);
+  float* xs = reinterpret_cast<float*>(mv_smem + tt * rowb);  // [groups][8 NT]: sums of x / kOut
+  float* part = xs + blocks * kSub * 8 * NT;                  // [tiles + WARPS - 1][8 NT][16]
   const int tiles = (p.N + 15) / 16;
-  const int row_bytes = (p.K + 31) / 32 * 16;
-  const int chunks = (p.K + kc - 1) / kc;
+  const int run0 = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.x / gridDim.x);
+  const int run1 = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
+  const int last_col = (p.K + 31) / 32 * 16 - 4 * VW;
+  const int last_g = (p.K - 1) >> p.group_shift;
+  const uint32_t ld_s = static_cast<uint32_t>(p.ld_s);
 
-  for (int tile_base = blockIdx.x; tile_base < tiles;
-       tile_base += chunks == 1 ? tiles : static_cast<int>(gridDim.x)) {
-    // with one chunk the loop below goes over all tiles of this block
-    const int my_tiles = chunks == 1 ? (tiles - tile_base + gridDim.x - 1) / gridDim.x : 1;
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    for (int ch = 0; ch < chunks; ++ch) {
-      const int k_lo = ch * kc, k_hi = min(p.K, k_lo + kc);
-      const int blocks = (k_hi - k_lo + 127) / 128;
-      const int per = (blocks + kMvWarps - 1) / kMvWarps;
-      const int total = per * my_tiles;
-      MvBlock<VW> buf[kMvDepth];
+  for (int r0 = run0; r0 < run1; r0 += kMvTiles) {
+    const int ntiles = min(kMvTiles, run1 - r0);
+    const int total = ntiles * blocks;
+    const int act = min(WARPS, total);  // warps with blocks
+    const int first = min(total * warp / act, total - 1);
+    const int left0 = warp < act ? total * (warp + 1) / act - first : 0;
 
-      auto fetch = [&](int it, MvBlock<VW>& b) {
-        const int tile = tile_base + (it / per) * static_cast<int>(gridDim.x);
-        const int blk = (it % per) * kMvWarps + warp;
-        const bool live = it < total && blk < blocks;
-        const int kb = k_lo / 128 + blk;
+    // The next block to fetch: its tile, its place in K and the lane's two
+    // rows.  Columns behind a row's end are read at its last words: x is 0
+    // there, and any weight will do.
+    MvBlock buf[kMvDepth];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = min(tile * 16 + g + 8 * h, p.N - 1);
-          const uint8_t* src = p.w + static_cast<int64_t>(row) * p.ld_w;
+    for (int d = 0; d < kMvDepth; ++d) buf[d].z[0] = buf[d].z[1] = 8;
+    int f_left = left0, f_tile = first / blocks, f_blk = first - f_tile * blocks;
+    const uint8_t* f_w[2];
+    const uint16_t* f_s[2];
+    int f_row[2];
+    auto rows_of = [&](int tile) {
 #pragma unroll
-          for (int sub = 0; sub < kSub; ++sub) {
-            const int at = kb * 64 + sub * 16 * VW + t4 * 4 * VW;
-            const bool in = live && at < row_bytes;
+      for (int h = 0; h < 2; ++h) {
+        f_row[h] = min((r0 + tile) * 16 + g + 8 * h, p.N - 1);
+        f_w[h] = p.w + f_row[h] * p.ld_w;
+        f_s[h] = p.s + f_row[h];
+      }
+    };
+    rows_of(f_tile);
+    auto fetch = [&](MvBlock& b) {
+      if (f_left > 0) {
+        --f_left;
+#pragma unroll
+        for (int sub = 0; sub < kSub; ++sub) {
+          const uint32_t col = min(f_blk * 64 + (sub * 16 + t4 * 4) * VW, last_col);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* src = f_w[h] + col;
             if constexpr (VW == 4) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (in) v = __ldcs(reinterpret_cast<const uint4*>(src + at));
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
               b.w[h][0] = v.x; b.w[h][1] = v.y; b.w[h][2] = v.z; b.w[h][3] = v.w;
             } else if constexpr (VW == 2) {
-              uint2 v = make_uint2(0, 0);
-              if (in) v = __ldg(reinterpret_cast<const uint2*>(src + at));
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
               b.w[h][2 * sub] = v.x; b.w[h][2 * sub + 1] = v.y;
             } else {
-              b.w[h][sub] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + at)) : 0u;
+              b.w[h][sub] = __ldg(reinterpret_cast<const uint32_t*>(src));
             }
-            const int k = kb * 128 + sub * 32 * VW;
-            const int64_t si = static_cast<int64_t>(k >> p.group_shift) * p.ld_s + row;
-            const bool sin = live && k < p.K;
-            b.s[h][sub] = sin ? __ldg(p.s + si) : static_cast<uint16_t>(0);
-            b.z[h][sub] = sin && p.z ? __ldg(p.z + si) : static_cast<uint8_t>(8);
           }
         }
-      };
-
+        const uint32_t gi = min(f_blk * kSub + (t4 & (kSub - 1)), last_g);
+        const uint64_t si = static_cast<uint64_t>(gi) * ld_s;
+        b.s[0] = __ldg(f_s[0] + si);
+        b.s[1] = __ldg(f_s[1] + si);
+        if (p.z) {
+          const uint8_t* z = p.z + si;
+          b.z[0] = __ldg(z + f_row[0]);
+          b.z[1] = __ldg(z + f_row[1]);
+        }
+        if (++f_blk == blocks) {
+          f_blk = 0;
+          rows_of(++f_tile);
+        }
+      }
+    };
 #pragma unroll
-      for (int d = 0; d < kMvDepth; ++d) fetch(d, buf[d]);
+    for (int d = 0; d < kMvDepth; ++d) fetch(buf[d]);
 
+    if (r0 == run0) {
       // x: chunks of eight values, zeros behind K; within a block of 32*VW
       // values chunk c lies at (c % VW) * 4 + c / VW, so that the four lanes
       // of a token read 64 neighbouring bytes
-      if (ch > 0 || tile_base != static_cast<int>(blockIdx.x)) __syncthreads();
       const int cpr = blocks * 16;
-      for (int u = tid; u < ntok * cpr; u += kMvThreads) {
-        const int r = u / cpr, c = u % cpr;
-        const int k = k_lo + c * 8;
-        const int left = min(8, p.K - k);
+      const int units = ntok * cpr;
+      int r = tid / cpr, c = tid - r * cpr;
+      for (int u0 = 0; u0 < units; u0 += kThreads) {
+        const bool live = u0 + tid < units;
+        const int k = c * 8;
+        const int left = live ? min(8, p.K - k) : 0;
         uint4 v = make_uint4(0, 0, 0, 0);
+        uint32_t* o = reinterpret_cast<uint32_t*>(&v);
         if (left > 0) {
-          const int64_t at = static_cast<int64_t>(t0 + r) * p.ld_x + k;
-          uint32_t* o = reinterpret_cast<uint32_t*>(&v);
+          const int64_t at = (t0 + r) * p.ld_x + k;
           if (X8) {
             const uint8_t* src = static_cast<const uint8_t*>(p.x) + at;
             uint32_t b[2] = {0, 0};
@@ -217,7 +270,7 @@ __global__ void __launch_bounds__(kMvThreads) w4_mv_kernel(const W4Args p, const
               for (int i = 0; i < 8; ++i)
                 if (i < left) b[i / 4] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i & 3));
             }
-            const uint2 lo = w4_from_e4m3<E>(b[0]), hi = w4_from_e4m3<E>(b[1]);
+            const uint2 lo = w4_from_e4m3<C>(b[0]), hi = w4_from_e4m3<C>(b[1]);
             v = make_uint4(lo.x, lo.y, hi.x, hi.y);
           } else {
             const uint16_t* src = static_cast<const uint16_t*>(p.x) + at;
@@ -230,92 +283,122 @@ __global__ void __launch_bounds__(kMvThreads) w4_mv_kernel(const W4Args p, const
             }
           }
         }
-        const int in = c & (4 * VW - 1);
-        const int at = (c - in) + (in % VW) * 4 + in / VW;
-        *reinterpret_cast<uint4*>(mv_smem + r * rowb + at * 16) = v;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = C::u32_to_f2(o[i]);
+          sum += f.x + f.y;
+          if (MvScale<C>::kX != 1.f)
+            o[i] = C::f2_to_u32(f.x * MvScale<C>::kX, f.y * MvScale<C>::kX);
+        }
+        // the 4*VW lanes of a group add their chunks
+#pragma unroll
+        for (int d = 2 * VW; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (live) {
+          const int in = c & (4 * VW - 1);
+          if (in == 0) xs[c / (4 * VW) * (8 * NT) + r] = sum * (1.f / MvScale<C>::kOut);
+          const int at = (c - in) + (in % VW) * 4 + in / VW;
+          *reinterpret_cast<uint4*>(mv_smem + r * rowb + at * 16) = v;
+        }
+        c += kThreads;
+        while (c >= cpr) {
+          c -= cpr;
+          ++r;
+        }
       }
-      __syncthreads();
+    }
+    __syncthreads();
 
-      const uint8_t* xr[NT];
-      bool xin[NT];
+    // columns of the product behind the last token repeat one and are not read
+    const uint8_t* xr[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        xin[n] = 8 * n + g < ntok;
-        xr[n] = mv_smem + (xin[n] ? 8 * n + g : 0) * rowb + t4 * 16;
-      }
+    for (int n = 0; n < NT; ++n) xr[n] = mv_smem + min(8 * n + g, ntok - 1) * rowb + t4 * 16;
 
-      for (int it0 = 0; it0 < total; it0 += kMvDepth) {
+    float acc[NT][4];
 #pragma unroll
-        for (int d = 0; d < kMvDepth; ++d) {
-          const int it = it0 + d;
-          if (it >= total) break;
-          const int blk = (it % per) * kMvWarps + warp;
-          if (blk < blocks) {
-            const MvBlock<VW>& b = buf[d];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int sub = 0; sub < kSub; ++sub) {
-              float gr[NT][4];
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    int left = left0, slot = first / blocks + warp, blk = first % blocks;
+    while (left > 0) {
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
+      for (int d = 0; d < kMvDepth; ++d) {
+        if (left <= 0) break;
+        const MvBlock& b = buf[d];
+        const uint32_t sz[2] = {b.s[0] | (b.z[0] << 16), b.s[1] | (b.z[1] << 16)};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) gr[n][i] = 0.f;
-              const uint32_t z0 = W4Magic<E>::zero(b.z[0][sub] & 15);
-              const uint32_t z1 = W4Magic<E>::zero(b.z[1][sub] & 15);
-#pragma unroll
-              for (int j = 0; j < VW; ++j) {
-                uint32_t a[4], c[4];
-                w4_pairs<E>(b.w[0][sub * VW + j], z0, a);
-                w4_pairs<E>(b.w[1][sub * VW + j], z1, c);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  uint4 xv = make_uint4(0, 0, 0, 0);
-                  if (xin[n])
-                    xv = *reinterpret_cast<const uint4*>(xr[n] + blk * 256 + (sub * VW + j) * 64);
-                  w4_mma<E>(gr[n], a[0], c[0], a[1], c[1], xv.x, xv.y);
-                  w4_mma<E>(gr[n], a[2], c[2], a[3], c[3], xv.z, xv.w);
-                }
-              }
-              const float s0 = E::bits_to_f32(b.s[0][sub]), s1 = E::bits_to_f32(b.s[1][sub]);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(s0, gr[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s0, gr[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s1, gr[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s1, gr[n][3], acc[n][3]);
-              }
-            }
+        for (int sub = 0; sub < kSub; ++sub) {
+          uint32_t sz0 = sz[0], sz1 = sz[1];
+          if (kSub > 1) {
+            sz0 = __shfl_sync(0xffffffffu, sz0, (lane & ~3) + sub);
+            sz1 = __shfl_sync(0xffffffffu, sz1, (lane & ~3) + sub);
           }
-          fetch(it + kMvDepth, buf[d]);
-          if (ch == chunks - 1 && it % per == per - 1) {
-            // the tile is done: add the warps' parts in their order
-            const int ti = it / per;
-            float* rb = red + (ti & 1) * (kMvWarps * NT * 128);
+          float g1[NT][4], g2[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g1[n][i] = g2[n][i] = 0.f;
+#pragma unroll
+          for (int j = 0; j < VW; ++j) {
+            constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;  // q, 16 q
+            const uint32_t a = b.w[0][sub * VW + j], e = b.w[1][sub * VW + j];
+            const uint32_t a8 = a >> 8, e8 = e >> 8;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float* w = rb + (warp * NT + n) * 128 + 2 * t4 * 16 + g;
-              w[0] = acc[n][0];
-              w[16] = acc[n][1];
-              w[8] = acc[n][2];
-              w[24] = acc[n][3];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+              const uint4 xv =
+                  *reinterpret_cast<const uint4*>(xr[n] + blk * 256 + (sub * VW + j) * 64);
+              w4_mma<C>(g1[n], a & kLo, e & kLo, a8 & kLo, e8 & kLo, xv.x, xv.z);
+              w4_mma<C>(g2[n], a & kHi, e & kHi, a8 & kHi, e8 & kHi, xv.y, xv.w);
             }
-            __syncthreads();
-            const int n0 = (tile_base + ti * static_cast<int>(gridDim.x)) * 16;
-            for (int e = tid; e < NT * 128; e += kMvThreads) {
-              const int tk = e >> 4, row = n0 + (e & 15);
-              if (tk < ntok && row < p.N) {
-                float v = 0.f;
+          }
+          const float s0 = E::bits_to_f32(static_cast<uint16_t>(sz0));
+          const float s1 = E::bits_to_f32(static_cast<uint16_t>(sz1));
+          const float z0 = -static_cast<float>((sz0 >> 16) & 15);
+          const float z1 = -static_cast<float>((sz1 >> 16) & 15);
 #pragma unroll
-                for (int w = 0; w < kMvWarps; ++w) v += rb[w * NT * 128 + e];
-                if (X8) v *= __ldg(p.x_scale + t0 + tk);
-                stg16(p.out + static_cast<int64_t>(t0 + tk) * p.ld_out + row, E::f32_to_bits(v));
-              }
-            }
+          for (int n = 0; n < NT; ++n) {
+            const float2 x2 = *reinterpret_cast<const float2*>(xs + (blk * kSub + sub) * (8 * NT) +
+                                                               8 * n + 2 * t4);
+            acc[n][0] = fmaf(s0, fmaf(z0, x2.x, fmaf(g2[n][0], 0.0625f, g1[n][0])), acc[n][0]);
+            acc[n][1] = fmaf(s0, fmaf(z0, x2.y, fmaf(g2[n][1], 0.0625f, g1[n][1])), acc[n][1]);
+            acc[n][2] = fmaf(s1, fmaf(z1, x2.x, fmaf(g2[n][2], 0.0625f, g1[n][2])), acc[n][2]);
+            acc[n][3] = fmaf(s1, fmaf(z1, x2.y, fmaf(g2[n][3], 0.0625f, g1[n][3])), acc[n][3]);
+          }
+        }
+        fetch(buf[d]);
+        --left;
+        if (++blk == blocks || left == 0) {
+          // this warp's part of a tile: slot = tile + warp, in the blocks' order
+          blk = 0;
+          float* o = part + slot++ * kPart + 2 * t4 * 16 + g;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n * 128] = acc[n][0];
+            o[n * 128 + 16] = acc[n][1];
+            o[n * 128 + 8] = acc[n][2];
+            o[n * 128 + 24] = acc[n][3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
           }
         }
       }
     }
+    __syncthreads();
+    for (int e = tid; e < ntiles * kPart; e += kThreads) {
+      const int tile = e / kPart, in = e % kPart;
+      const int tk = in >> 4, row = (r0 + tile) * 16 + (in & 15);
+      if (tk < ntok && row < p.N) {
+        // the warps that hold the tile's first and last block
+        const int w0 = (tile * blocks * act + act - 1) / total;
+        const int w1 = ((tile + 1) * blocks * act - 1) / total;
+        float v = 0.f;
+        for (int w = w0; w <= w1; ++w) v += part[(tile + w) * kPart + in];
+        v *= MvScale<C>::kOut;
+        if (X8) v *= __ldg(p.x_scale + t0 + tk);
+        stg16(p.out + (t0 + tk) * p.ld_out + row, E::f32_to_bits(v));
+      }
+    }
+    if (r0 + kMvTiles < run1) __syncthreads();
   }
 }
 

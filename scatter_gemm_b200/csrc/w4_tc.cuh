@@ -6,16 +6,23 @@
 // A tile is 128 weight rows x NT tokens; the weight rows are the rows of the
 // MMA, so that a weight's row is a lane of tensor memory (TMEM) and its scale a
 // scalar of the thread that owns the lane.  K goes in blocks of 128:
-//  - one thread loads the block's packed weights (8 KB) and x tile by TMA;
-//  - the widening warps turn each packed row into q - z in the element type of
-//    x (exact: bf16, fp16, or e4m3 scaled by 2^-6) and store it to TMEM, from
-//    where the MMA reads it: neither the widened weights' stores nor their
-//    loads by the MMA take shared-memory bandwidth;
-//  - one thread issues the MMAs of a group into one of two accumulators;
+//  - one warp loads the block's packed weights (8 KB) and x tile by TMA;
+//  - sets of four widening warps, a block each in turn, turn the packed rows
+//    into q - z in the element type of x (exact: bf16, fp16, or e4m3 scaled by
+//    2^-6) and store them to TMEM, from where the MMA reads them: neither the
+//    widened weights' stores nor their loads by the MMA take shared-memory
+//    bandwidth;
+//  - two warps issue the MMAs, a group each in turn, into a ring of
+//    accumulators;
 //  - the scaling warps add each group's accumulator, times its scale, to fp32
-//    sums in registers, while the next group is multiplied into the other.
+//    sums in registers.
 // So the weights are never rounded, and a scale costs one fused multiply-add
-// for each group and output instead of a multiplication for each weight.
+// for each group and output instead of a multiplication for each weight.  One
+// block of threads an SM, most of an SM's shared memory and all of its TMEM.
+//
+// A role's own path through a block, its barriers above all, takes 500 to 1200
+// cycles, the block's data 340 (8 KB at an SM's share of the memory
+// bandwidth): hence the sets of widening warps and the two MMA warps.
 //
 // With few tiles the K range is split over a thread-block cluster; the parts
 // are added in rank order through distributed shared memory.
@@ -106,31 +113,61 @@ __device__ __forceinline__ void w4_bytes8(uint32_t w, const uint4& T, uint32_t& 
   b += b & 0x40404040u;
 }
 
-// NT: tokens of a tile.  GS: log2 of the group size.  NW: widening warps and
-// scaling warps each (4 or 8; with 8 the scaling warps split the tokens).
-template <class E, bool X8, int NT, int GS, int NW>
+// A role's place in a ring of n buffers: the buffer, and the parity of the
+// phase in which it is filled (`fill`) or was last drained (`drain`; a fresh
+// barrier passes a wait for parity 1).
+struct RingPos {
+  int i = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ uint32_t fill() const { return ph; }
+  __device__ __forceinline__ uint32_t drain() const { return ph ^ 1u; }
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) {
+      i = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
+}
+
+// NT: tokens of a tile.  GS: log2 of the group size.  SETS: sets of four
+// widening warps.  SW: scaling warps, four, or eight that split the tokens.
+template <bool X8, int NT, int GS, int SETS, int SW>
 struct W4Tc {
-  static constexpr int kThreads = 64 * NW + 64;
+  static constexpr int kWide = 4 * SETS;                        // widening warps
+  static constexpr int kTmaWarp = kWide + SW, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (kWide + SW + 3);
   static constexpr int kGroups = 128 >> GS;                     // groups of a block
   static constexpr int kACols = X8 ? 32 : 64;                   // TMEM columns of a widened block
-  static constexpr int kTmem = NT > 64 ? 512 : 256;
-  static constexpr int kABufs = (kTmem - 2 * NT) / kACols >= 4 ? 4 : (kTmem - 2 * NT) / kACols;
+  static constexpr int kTmem = 512;
+  static constexpr int kDBufs = NT <= 64 ? 4 : 2;               // accumulators
+  static constexpr int kAFit = (kTmem - kDBufs * NT) / kACols;
+  // A buffer of a ring belongs to one set and one MMA warp for good: one that
+  // waits on it has then seen all of its earlier phases, and cannot take the
+  // parity of a phase two back for its own.  So the rings' lengths are
+  // multiples of the sets' and the MMA warps' numbers.
+  static constexpr int kRing = SETS % 2 ? 2 * SETS : SETS;
+  static constexpr int kABufs = (kAFit < 8 ? kAFit : 8) / kRing * kRing;
   static constexpr int kWBytes = kW4M * 64;
   static constexpr int kXBytes = NT * (X8 ? 128 : 256);
   static constexpr int kStage = kWBytes + kXBytes;
-  static constexpr int kCols = NT / (NW / 4);                   // tokens of a scaling warp
-  static constexpr int kMinBlocks = NW == 4 ? 2 : 1;
-  static_assert(kABufs >= 2, "two widened blocks at least");
+  static constexpr int kCols = NT / (SW / 4);                   // tokens of a scaling warp
+  static constexpr int kMmaArrive = kGroups > 1 ? 2 : 1;        // MMA warps that share a block
+  static_assert(kABufs >= kRing, "a widened block for each set");
 };
 
-template <class E, bool X8, int NT, int GS, int NW>
-__global__ void __launch_bounds__((W4Tc<E, X8, NT, GS, NW>::kThreads),
-                                  (W4Tc<E, X8, NT, GS, NW>::kMinBlocks))
+template <class E, bool X8, int NT, int GS, int SETS, int SW>
+__global__ void __launch_bounds__((W4Tc<X8, NT, GS, SETS, SW>::kThreads), 1)
 w4_tc_kernel(const __grid_constant__ W4TcParams P) {
-  using C = W4Tc<E, X8, NT, GS, NW>;
+  using C = W4Tc<X8, NT, GS, SETS, SW>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const W4Args& p = P.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -142,21 +179,22 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   const uint32_t afull0 = empty0 + 8 * P.stages;
   const uint32_t aempty0 = afull0 + 8 * C::kABufs;
   const uint32_t dfull0 = aempty0 + 8 * C::kABufs;
-  const uint32_t dempty0 = dfull0 + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * P.stages + 2 * C::kABufs + 4);
+  const uint32_t dempty0 = dfull0 + 8 * C::kDBufs;
+  uint32_t* tmem_slot =
+      reinterpret_cast<uint32_t*>(bars + 2 * P.stages + 2 * C::kABufs + 2 * C::kDBufs);
 
   if (tid == 0) {
     for (int s = 0; s < P.stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, NW + 1);  // the widening warps and the MMAs
+      mbar_init(empty0 + 8 * s, 4 + C::kMmaArrive);  // a set of widening warps and the MMAs
     }
     for (int s = 0; s < C::kABufs; ++s) {
-      mbar_init(afull0 + 8 * s, NW);
-      mbar_init(aempty0 + 8 * s, 1);
+      mbar_init(afull0 + 8 * s, 4);
+      mbar_init(aempty0 + 8 * s, C::kMmaArrive);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::kDBufs; ++s) {
       mbar_init(dfull0 + 8 * s, 1);
-      mbar_init(dempty0 + 8 * s, NW);
+      mbar_init(dempty0 + 8 * s, SW);
     }
     fence_mbar_init();
   }
@@ -166,156 +204,167 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     for (int i = 0; i < 4; ++i) c |= w4_code8(4 * (tid & 3) + i, tid >> 2) << (8 * i);
     reinterpret_cast<uint32_t*>(codes)[tid] = c;
   }
-  if (warp == 2 * NW) {
+  if (warp == C::kTmaWarp) {
     if (lane == 0) {
       tma_prefetch_desc(&P.tmap_w);
       tma_prefetch_desc(&P.tmap_x);
     }
-  } else if (warp == 2 * NW + 1) {
+  } else if (warp == C::kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t abase = tmem + 2 * NT;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t abase = tmem + C::kDBufs * NT;
   const int rank = P.cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(P.nkb) * rank / P.cs);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(P.nkb) * (rank + 1) / P.cs);
+  const int kb0 = P.nkb * rank / P.cs, kb1 = P.nkb * (rank + 1) / P.cs;
   const int tiles = P.tiles_n * P.tiles_t;
   const int first = blockIdx.x / P.cs, step = gridDim.x / P.cs;
   bool ok = true;
 
-  if (warp < NW) {
+  if (warp < C::kWide) {
     // =========================== widening: a lane of TMEM, and a row, a thread
-    const int quad = warp & 3;
+    const int quad = warp & 3, set = warp >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t rsw = (row >> 1) & 3;
-    constexpr int kHalves = NW == 4 ? 2 : 1;
-    const int h0 = NW == 4 ? 0 : warp >> 2;
-    int it = 0;
+    // this set's blocks, every SETS-th of the CTA's, counted over its tiles
+    RingPos st, ab;
+    for (int i = 0; i < set; ++i) {
+      st.next(P.stages);
+      ab.next(C::kABufs);
+    }
+    int skip = set;  // blocks of the next tile before this set's first
     for (int tile = first; tile < tiles && ok; tile += step) {
       const int n = (tile % P.tiles_n) * kW4M + row;
       const bool zin = p.z != nullptr && n < p.N;
-      // the zero points of a block, a byte each, four blocks ahead
-      auto zeros = [&](int kb) {
-        uint32_t v = 0x08080808u;
-        if (zin && kb < kb1) {
-          v = 0;
+      // the zero points of a block, some blocks ahead.  They stay as loaded,
+      // each in a register of its own: arithmetic on a value that is on its
+      // way, even moving it, would wait for it.
+      constexpr int kAhead = SETS > 2 ? 2 : 4;
+      uint32_t zq[kAhead][C::kGroups];
+      auto zeros = [&](int kb, uint32_t (&v)[C::kGroups]) {
 #pragma unroll
-          for (int i = 0; i < C::kGroups; ++i) {
-            const int gi = kb * C::kGroups + i;
-            if ((gi << GS) < p.K)
-              v |= static_cast<uint32_t>(__ldg(p.z + gi * p.ld_s + n) & 15) << (8 * i);
-          }
+        for (int i = 0; i < C::kGroups; ++i) {
+          const int gi = kb * C::kGroups + i;
+          if (zin && kb < kb1 && (gi << GS) < p.K) v[i] = __ldg(p.z + gi * p.ld_s + n);
         }
-        return v;
       };
-      uint32_t zq[4];
+      int kb = kb0 + skip;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) zq[i] = zeros(kb0 + i);
-      for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-        const uint32_t z4 = zq[0];
-        zq[0] = zq[1]; zq[1] = zq[2]; zq[2] = zq[3];
-        zq[3] = zeros(kb + 4);
-        const int s = it % P.stages;
-        ok = mbar_wait(full0 + 8 * s, (it / P.stages) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* src = smem + s * C::kStage + row * 64;
-        uint4 pk[2 * kHalves];
+      for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int c = 0; c < 2 * kHalves; ++c)
-          pk[c] = *reinterpret_cast<const uint4*>(src + (((2 * h0 + c) ^ rsw) << 4));
-        const int ab = it % C::kABufs;
-        if (it >= C::kABufs) ok = mbar_wait(aempty0 + 8 * ab, (it / C::kABufs - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t dst = abase + lane_off + ab * C::kACols;
+        for (int i = 0; i < C::kGroups; ++i) zq[u][i] = 8;
+        zeros(kb + u * SETS, zq[u]);
+      }
+      while (kb < kb1 && ok) {
 #pragma unroll
-        for (int c = 0; c < 2 * kHalves; ++c) {
-          // 32 weights, one group at most
-          const int c4 = 2 * h0 + c;
-          const int z = (z4 >> (8 * ((c4 * 32) >> GS))) & 15;
-          const uint32_t w[4] = {pk[c].x, pk[c].y, pk[c].z, pk[c].w};
+        for (int u = 0; u < kAhead; ++u) {
+          if (kb >= kb1 || !ok) break;
+          ok = mbar_wait(full0 + 8 * st.i, st.fill());
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* src = smem + st.i * C::kStage + row * 64;
+          uint4 pk[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) pk[c] = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
+          ok = mbar_wait(aempty0 + 8 * ab.i, ab.drain());
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t dst = abase + lane_off + ab.i * C::kACols;
           if constexpr (X8) {
-            if (c & 1) continue;
-            const int z2 = (z4 >> (8 * (((c4 + 1) * 32) >> GS))) & 15;
-            const uint32_t w2[4] = {pk[c + 1].x, pk[c + 1].y, pk[c + 1].z, pk[c + 1].w};
-            const uint4 T = codes[z], T2 = codes[z2];
-            uint32_t r[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w4_bytes8(w[j], T, r[2 * j], r[2 * j + 1]);
-              w4_bytes8(w2[j], T2, r[8 + 2 * j], r[9 + 2 * j]);
+            for (int c = 0; c < 4; c += 2) {
+              uint32_t r[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w[4] = {pk[c + h].x, pk[c + h].y, pk[c + h].z, pk[c + h].w};
+                const uint4 T = codes[zq[u][((c + h) * 32) >> GS] & 15];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w4_bytes8(w[j], T, r[8 * h + 2 * j], r[8 * h + 2 * j + 1]);
+              }
+              tmem_st16(dst + c * 8, r);
             }
-            tmem_st16(dst + c4 * 8, r);
           } else {
-            const uint32_t zz = W4Magic<E>::zero(z);
-            uint32_t r[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t q[4];
-              w4_pairs<E>(w[j], zz, q);
-              r[4 * j] = q[0]; r[4 * j + 1] = q[1]; r[4 * j + 2] = q[2]; r[4 * j + 3] = q[3];
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t w[4] = {pk[c].x, pk[c].y, pk[c].z, pk[c].w};
+              const uint32_t zz = W4Magic<E>::zero(zq[u][(c * 32) >> GS] & 15);
+              uint32_t r[16];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t q[4];
+                w4_pairs<E>(w[j], zz, q);
+                r[4 * j] = q[0]; r[4 * j + 1] = q[1]; r[4 * j + 2] = q[2]; r[4 * j + 3] = q[3];
+              }
+              tmem_st16(dst + c * 16, r);
             }
-            tmem_st16(dst + c4 * 16, r);
           }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(afull0 + 8 * ab);
-          mbar_arrive(empty0 + 8 * s);
+          zeros(kb + kAhead * SETS, zq[u]);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(afull0 + 8 * ab.i);
+            mbar_arrive(empty0 + 8 * st.i);
+          }
+#pragma unroll
+          for (int i = 0; i < SETS; ++i) {
+            st.next(P.stages);
+            ab.next(C::kABufs);
+          }
+          kb += SETS;
         }
       }
+      skip = kb - kb1;
     }
-  } else if (warp < 2 * NW) {
+  } else if (warp < C::kTmaWarp) {
     // =========================== scaling: sum += scale * accumulator, then the output
-    const int w = warp - NW, quad = w & 3;
+    const int w = warp - C::kWide, quad = w & 3;
     const int row = quad * 32 + lane;
     const int col0 = (w >> 2) * C::kCols;
     const uint32_t dsrc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
-    int gi = 0;
+    RingPos db;
     for (int tile = first; tile < tiles; tile += step) {
       const int n = (tile % P.tiles_n) * kW4M + row;
       const int tb = (tile / P.tiles_n) * NT;
       const int g0 = kb0 * C::kGroups, g1 = kb1 * C::kGroups;
-      auto scale_of = [&](int g) {
-        return n < p.N && g < g1 && (g << GS) < p.K
-                   ? E::bits_to_f32(__ldg(p.s + g * p.ld_s + n))
-                   : 0.f;
+      // a group's scale, four groups ahead, as loaded
+      auto scale_of = [&](int g) -> uint16_t {
+        return n < p.N && g < g1 && (g << GS) < p.K ? __ldg(p.s + g * p.ld_s + n) : uint16_t(0);
       };
       float acc[C::kCols];
 #pragma unroll
       for (int c = 0; c < C::kCols; ++c) acc[c] = 0.f;
-      float sq[4];
+      uint16_t sq[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sq[i] = scale_of(g0 + i);
-      for (int g = g0; g < g1 && ok; ++g, ++gi) {
-        const float sc = X8 ? sq[0] * 64.f : sq[0];
-        sq[0] = sq[1]; sq[1] = sq[2]; sq[2] = sq[3];
-        sq[3] = scale_of(g + 4);
-        const int db = gi & 1;
-        ok = mbar_wait(dfull0 + 8 * db, (gi >> 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
+      for (int u = 0; u < 4; ++u) sq[u] = scale_of(g0 + u);
+      for (int g = g0; g < g1 && ok; g += 4) {
 #pragma unroll
-        for (int c = 0; c < C::kCols; c += 16) {
-          float v[16];
-          tmem_ld16(dsrc + db * NT + c, v);
-          tmem_ld_wait();
+        for (int u = 0; u < 4; ++u) {
+          if (g + u >= g1 || !ok) break;
+          ok = mbar_wait(dfull0 + 8 * db.i, db.fill());
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const float sc = X8 ? E::bits_to_f32(sq[u]) * 64.f : E::bits_to_f32(sq[u]);
+          sq[u] = scale_of(g + u + 4);
+          tc_fence_after();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(sc, v[i], acc[c + i]);
+          for (int c = 0; c < C::kCols; c += 16) {
+            float v[16];
+            tmem_ld16(dsrc + db.i * NT + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(sc, v[i], acc[c + i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dempty0 + 8 * db.i);
+          db.next(C::kDBufs);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dempty0 + 8 * db);
       }
       if (!ok) break;
       if (P.cs == 1) {
@@ -337,65 +386,81 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
         for (int c = 0; c < C::kCols; ++c) part[(col0 + c) * kW4M + row] = acc[c];
       }
     }
-  } else if (warp == 2 * NW) {
+  } else if (warp == C::kTmaWarp) {
     // =========================== TMA
-    if (lane == 0) {
-      int it = 0;
-      for (int tile = first; tile < tiles && ok; tile += step) {
-        const int n0 = (tile % P.tiles_n) * kW4M, tb = (tile / P.tiles_n) * NT;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % P.stages;
-          if (it >= P.stages) ok = mbar_wait(empty0 + 8 * s, (it / P.stages - 1) & 1);
-          if (!ok) break;
-          const uint32_t dst = sbase + s * C::kStage, bar = full0 + 8 * s;
+    RingPos st;
+    int issued = 0;
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      const int n0 = (tile % P.tiles_n) * kW4M, tb = (tile / P.tiles_n) * NT;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = mbar_wait(empty0 + 8 * st.i, st.drain());
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = sbase + st.i * C::kStage, bar = full0 + 8 * st.i;
+        if (elect_one()) {
           mbar_arrive_expect_tx(bar, C::kStage);
           tma_load_2d(dst, &P.tmap_w, bar, kb * 64, n0);
           tma_load_2d(dst + C::kWBytes, &P.tmap_x, bar, kb * kW4K, tb);
           if (!X8) tma_load_2d(dst + C::kWBytes + NT * 128, &P.tmap_x, bar, kb * kW4K + 64, tb);
         }
+        __syncwarp();
+        st.next(P.stages);
+        ++issued;
       }
-      // after a wait that gave up: the copies still in flight
-      if (!ok)
-        for (int i = it < P.stages ? 0 : it - P.stages; i < it; ++i)
-          mbar_wait(full0 + 8 * (i % P.stages), (i / P.stages) & 1);
     }
-    __syncwarp();
+    // after a wait that gave up: the copies still in flight
+    if (!ok)
+      for (int i = max(0, issued - P.stages); i < issued; ++i)
+        mbar_wait(full0 + 8 * (i % P.stages), (i / P.stages) & 1);
   } else {
-    // =========================== MMA
-    if (lane == 0) {
-      int it = 0, gi = 0;
-      for (int tile = first; tile < tiles && ok; tile += step) {
-        for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-          const int s = it % P.stages, ab = it % C::kABufs;
-          ok = mbar_wait(full0 + 8 * s, (it / P.stages) & 1) &&
-               mbar_wait(afull0 + 8 * ab, (it / C::kABufs) & 1);
-          const uint32_t xs = sbase + s * C::kStage + C::kWBytes;
-          constexpr int kSteps = X8 ? 4 : 8;           // MMAs of a block
-          constexpr int kPer = kSteps / C::kGroups;    // MMAs of a group
+    // =========================== MMA: group i of the CTA is warp i % 2's
+    const int mw = warp - C::kMmaWarp;
+    constexpr int kSteps = X8 ? 4 : 8;           // MMAs of a block
+    constexpr int kPer = kSteps / C::kGroups;    // MMAs of a group
+    const uint64_t bd0 = make_sdesc(sbase + C::kWBytes, 128, 2);
+    const uint32_t idesc = P.idesc;
+    RingPos st, ab, db;
+    uint32_t blk = 0;
+    for (int tile = first; tile < tiles && ok; tile += step) {
+      for (int kb = kb0; kb < kb1 && ok; ++kb, ++blk) {
+        if (C::kGroups > 1 || (blk & 1) == static_cast<uint32_t>(mw)) {
+          ok = mbar_wait(full0 + 8 * st.i, st.fill()) && mbar_wait(afull0 + 8 * ab.i, ab.fill());
+          // addresses in a descriptor are in units of 16 bytes
+          const uint64_t bd = bd0 + static_cast<uint32_t>(st.i * (C::kStage / 16));
+          const uint32_t at = abase + ab.i * C::kACols;
 #pragma unroll
-          for (int j = 0; j < C::kGroups && ok; ++j, ++gi) {
-            const int db = gi & 1;
-            if (gi >= 2) ok = mbar_wait(dempty0 + 8 * db, ((gi >> 1) - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
+          for (int j = 0; j < C::kGroups; ++j) {
+            if (C::kGroups == 1 || (j & 1) == mw) {
+              ok = ok && mbar_wait(dempty0 + 8 * db.i, db.drain());
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              const int kk = j * kPer + i;
-              const uint64_t bd = make_sdesc(xs + (kk / 4) * NT * 128 + (kk % 4) * 32, 128, 2);
-              tc_mma_ts<X8>(tmem + db * NT, abase + ab * C::kACols + kk * 8, bd, P.idesc,
-                            i > 0 ? 1u : 0u);
+                for (int i = 0; i < kPer; ++i) {
+                  const int kk = j * kPer + i;
+                  tc_mma_ts<X8>(tmem + db.i * NT, at + kk * 8,
+                                bd + (kk / 4) * (NT * 8) + (kk % 4) * 2, idesc, i > 0 ? 1u : 0u);
+                }
+                if (j + C::kMmaArrive >= C::kGroups) {  // this warp's last group of the block
+                  tc_commit(aempty0 + 8 * ab.i);
+                  tc_commit(empty0 + 8 * st.i);
+                }
+                tc_commit(dfull0 + 8 * db.i);
+              }
+              __syncwarp();
             }
-            if (j == C::kGroups - 1) {
-              tc_commit(aempty0 + 8 * ab);
-              tc_commit(empty0 + 8 * s);
-            }
-            tc_commit(dfull0 + 8 * db);
+            db.next(C::kDBufs);
           }
+        } else {
+          db.next(C::kDBufs);
         }
+        st.next(P.stages);
+        ab.next(C::kABufs);
       }
     }
-    __syncwarp();
   }
+  __syncwarp();
 
   if (P.cs > 1) {
     // one tile: the parts of the cluster's CTAs, each CTA adding its share of
@@ -403,7 +468,6 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     ok = __syncthreads_and(ok);
     cluster_sync();
     const int tb = (first / P.tiles_n) * NT, n0 = (first % P.tiles_n) * kW4M;
-    const uint32_t mine = sbase;
     const int c0 = NT * rank / P.cs, c1 = NT * (rank + 1) / P.cs;
     for (int e = tid; e < (c1 - c0) * kW4M; e += C::kThreads) {
       const int c = c0 + e / kW4M, r = e % kW4M;
@@ -411,7 +475,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
       if (t < p.tok && n < p.N && ok) {
         float v = 0.f;
         for (int i = 0; i < P.cs; ++i)
-          v += ld_dsmem_f32(mapa_shared(mine + static_cast<uint32_t>(c * kW4M + r) * 4, i));
+          v += ld_dsmem_f32(mapa_shared(sbase + static_cast<uint32_t>(c * kW4M + r) * 4, i));
         if (X8) v *= __ldg(p.x_scale + t);
         stg16(p.out + t * p.ld_out + n, E::f32_to_bits(v));
       }
@@ -419,7 +483,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     cluster_sync_relaxed();
   }
   __syncthreads();
-  if (warp == 2 * NW + 1) {
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
