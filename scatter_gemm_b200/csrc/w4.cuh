@@ -77,27 +77,42 @@ __device__ __forceinline__ uint2 w4_from_e4m3(uint32_t b) {
   return make_uint2(E::f2_to_u32(f.x, f.y), E::f2_to_u32(g.x, g.y));
 }
 
-// C += A (16 x 16, rows of weights) * B (16 x 8, columns of tokens).
+// C = A (16 x 16, rows of weights) * B (16 x 8, columns of tokens) where
+// `fresh`, else C += that.
 template <class E>
 __device__ __forceinline__ void w4_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                       uint32_t a3, uint32_t b0, uint32_t b1);
+                                       uint32_t a3, uint32_t b0, uint32_t b1, bool fresh);
 template <>
 __device__ __forceinline__ void w4_mma<Bf16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                             uint32_t a3, uint32_t b0, uint32_t b1, bool fresh) {
+  if (fresh)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 template <>
 __device__ __forceinline__ void w4_mma<Fp16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                             uint32_t a3, uint32_t b0, uint32_t b1, bool fresh) {
+  if (fresh)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // What turns packed weights into operands of w4_mv without arithmetic: the bit
@@ -298,7 +313,8 @@ w4_mv_kernel(const W4Args p, const int tt) {
           const int in = c & (4 * VW - 1);
           if (in == 0) xs[c / (4 * VW) * (8 * NT) + r] = sum * (1.f / MvScale<C>::kOut);
           const int at = (c - in) + (in % VW) * 4 + in / VW;
-          *reinterpret_cast<uint4*>(mv_smem + r * rowb + at * 16) = v;
+          // a product takes pairs 0 and 2 or 1 and 3 of a word: neighbours here
+          *reinterpret_cast<uint4*>(mv_smem + r * rowb + at * 16) = make_uint4(v.x, v.z, v.y, v.w);
         }
         c += kThreads;
         while (c >= cpr) {
@@ -335,10 +351,6 @@ w4_mv_kernel(const W4Args p, const int tt) {
           }
           float g1[NT][4], g2[NT][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g1[n][i] = g2[n][i] = 0.f;
-#pragma unroll
           for (int j = 0; j < VW; ++j) {
             constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;  // q, 16 q
             const uint32_t a = b.w[0][sub * VW + j], e = b.w[1][sub * VW + j];
@@ -347,8 +359,8 @@ w4_mv_kernel(const W4Args p, const int tt) {
             for (int n = 0; n < NT; ++n) {
               const uint4 xv =
                   *reinterpret_cast<const uint4*>(xr[n] + blk * 256 + (sub * VW + j) * 64);
-              w4_mma<C>(g1[n], a & kLo, e & kLo, a8 & kLo, e8 & kLo, xv.x, xv.z);
-              w4_mma<C>(g2[n], a & kHi, e & kHi, a8 & kHi, e8 & kHi, xv.y, xv.w);
+              w4_mma<C>(g1[n], a & kLo, e & kLo, a8 & kLo, e8 & kLo, xv.x, xv.y, j == 0);
+              w4_mma<C>(g2[n], a & kHi, e & kHi, a8 & kHi, e8 & kHi, xv.z, xv.w, j == 0);
             }
           }
           const float s0 = E::bits_to_f32(static_cast<uint16_t>(sz0));
