@@ -9,10 +9,15 @@
 #include "w4_tc.cuh"
 
 #include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #ifndef LORA_W4_MV_TOKENS
 #define LORA_W4_MV_TOKENS 16 // 4-bit projection: tokens up to which w4_mv runs
+#endif
+
+#ifndef LORA_ROPE_STEPS
+#define LORA_ROPE_STEPS 4
 #endif
 
 namespace {
@@ -104,6 +109,70 @@ extern "C" lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* res
 
 // ------------------------------------------------------------------ rotate and append
 
+namespace {
+
+template <class E, bool C8, bool INTER, bool NORM, int STEPS>
+void launch_rope(const lora::RopeAppendArgs& a, int lg, unsigned grid, int wpt, cudaStream_t st) {
+  if (lg == 4)
+    lora::rope_append_kernel<E, C8, INTER, NORM, 4, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+  else if (lg == 8)
+    lora::rope_append_kernel<E, C8, INTER, NORM, 8, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+  else if (lg == 16)
+    lora::rope_append_kernel<E, C8, INTER, NORM, 16, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+  else
+    lora::rope_append_kernel<E, C8, INTER, NORM, 32, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+}
+
+template <class E, bool C8, bool INTER, bool NORM>
+lora_status rope_pieces(const lora::RopeAppendArgs& a, cudaStream_t st) {
+  int lg = 4;
+  while (lg < a.D / 16) lg *= 2;
+  const int all = ((a.hq + 2 * a.hkv) * lg + 31) / 32;  // steps of a token
+  // Beyond two steps for each warp that an SM holds, a warp takes four.
+  const bool many = all > 1 && static_cast<int64_t>(a.tok) * all > 148 * 64 * 2;
+  const int wpt = many ? (all + LORA_ROPE_STEPS - 1) / LORA_ROPE_STEPS : all;
+  const int64_t grid = (static_cast<int64_t>(a.tok) * wpt + 7) / 8;
+  if (grid >= (int64_t(1) << 28)) return LORA_ERR_UNSUPPORTED;
+  const unsigned g = static_cast<unsigned>(grid);
+  if (many) launch_rope<E, C8, INTER, NORM, LORA_ROPE_STEPS>(a, lg, g, wpt, st);
+  else launch_rope<E, C8, INTER, NORM, 1>(a, lg, g, wpt, st);
+  return LORA_OK;
+}
+
+template <class E, bool C8>
+lora_status rope_append(const lora::RopeAppendArgs& a, cudaStream_t st) {
+  const int heads = a.hq + 2 * a.hkv;
+  auto mul = [](int64_t m, std::initializer_list<int64_t> v) {
+    for (int64_t x : v)
+      if (x % m) return false;
+    return true;
+  };
+  const int cb = C8 ? 8 : 16;  // bytes of a piece of the cache
+  const bool pieces =
+      a.D % 16 == 0 && (a.R % 16 == 0 || a.interleaved) && aligned_to(a.qkv, 16) &&
+      mul(8, {a.ld_qkv, a.off_q, a.off_k, a.off_v, a.ld_q, a.k_page, a.k_slot, a.k_head, a.v_page,
+              a.v_slot, a.v_head}) &&
+      aligned_to(a.q_out, 16) && aligned_to(a.kc, cb) && aligned_to(a.vc, cb) &&
+      aligned_to(a.qw, 16) && aligned_to(a.kw, 16);
+  if (pieces) {
+    const lora_status s = a.interleaved
+                              ? (a.qw ? rope_pieces<E, C8, true, true>(a, st)
+                                      : rope_pieces<E, C8, true, false>(a, st))
+                              : (a.qw ? rope_pieces<E, C8, false, true>(a, st)
+                                      : rope_pieces<E, C8, false, false>(a, st));
+    if (s != LORA_OK) return s;
+  } else {
+    const int64_t grid = (static_cast<int64_t>(a.tok) * heads + 7) / 8;
+    if (grid >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
+    lora::rope_append_general_kernel<E, C8><<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
+  }
+  ++g_launches;
+  g_last_path = LORA_PATH_GENERAL;
+  return launch_status();
+}
+
+}  // namespace
+
 extern "C" lora_status lora_rope_append(
     const void* qkv, int64_t ld_qkv, const int32_t* qkv_offsets, int head_dim, int rotary_dim,
     const void* positions, int64_t ld_pos, int axes, const uint8_t* axis_map,
@@ -185,20 +254,10 @@ extern "C" lora_status lora_rope_append(
   a.interleaved = interleaved;
   a.idx64 = index_bytes == 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t warps = static_cast<int64_t>(tok) * (a.hq + 2 * a.hkv);
-  if ((warps + 7) / 8 >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
   const bool c8 = cache_dtype == LORA_E4M3;
-  if (dtype == LORA_BF16) {
-    if (c8) lora::rope_append_general_kernel<lora::Bf16, true><<<grid, 256, 0, st>>>(a);
-    else lora::rope_append_general_kernel<lora::Bf16, false><<<grid, 256, 0, st>>>(a);
-  } else {
-    if (c8) lora::rope_append_general_kernel<lora::Fp16, true><<<grid, 256, 0, st>>>(a);
-    else lora::rope_append_general_kernel<lora::Fp16, false><<<grid, 256, 0, st>>>(a);
-  }
-  ++g_launches;
-  g_last_path = LORA_PATH_GENERAL;
-  return launch_status();
+  if (dtype == LORA_BF16)
+    return c8 ? rope_append<lora::Bf16, true>(a, st) : rope_append<lora::Bf16, false>(a, st);
+  return c8 ? rope_append<lora::Fp16, true>(a, st) : rope_append<lora::Fp16, false>(a, st);
 }
 
 // ------------------------------------------------------------------ 4-bit base projection

@@ -56,7 +56,8 @@ __device__ __forceinline__ int64_t rope_position(const RopeAppendArgs& p, int ax
   return v < 0 ? 0 : (v >= p.max_pos ? p.max_pos - 1 : v);
 }
 
-// Any head size, stride and alignment: one warp a head, one pair a lane.
+// Any head size, stride and alignment: one warp a head, one pair a lane.  Runs
+// where rope_append_kernel cannot: see its conditions.
 template <class E, bool C8>
 __global__ void __launch_bounds__(256) rope_append_general_kernel(const RopeAppendArgs p) {
   const int lane = threadIdx.x & 31;
@@ -113,6 +114,217 @@ __global__ void __launch_bounds__(256) rope_append_general_kernel(const RopeAppe
     put(eb, b * c + a * s);
   }
   for (int e = 2 * half + lane; e < p.D; e += 32) put(e, get(e));
+}
+
+// Eight elements as floats, and back.
+template <class E>
+__device__ __forceinline__ void rope_unpack(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = E::u32_to_f2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+template <class E>
+__device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
+  return make_uint4(E::f2_to_u32(f[0], f[1]), E::f2_to_u32(f[2], f[3]), E::f2_to_u32(f[4], f[5]),
+                    E::f2_to_u32(f[6], f[7]));
+}
+
+// Heads of whole 16-byte pieces: 16-byte aligned rows, heads and cache entries
+// (8-byte with an 8-bit cache), head_dim a multiple of 16 and, unless
+// interleaved, R too.
+//
+// A group of LG lanes (a power of two, at least head_dim / 16) takes a head:
+// each lane eight neighbouring frequencies, that is two 16-byte pieces of the
+// head, R/2 apart, or next to each other when interleaved or behind the
+// rotated part; so a pair never leaves its lane and a head's norm is a few
+// shuffles.  A warp takes 32 / LG heads of one token at a time, STEPS times,
+// all of its loads first: with many tokens that keeps enough bytes under way
+// and reads the token's cosines and sines once for STEPS steps.
+template <class E, bool C8, bool INTER, bool NORM, int LG, int STEPS>
+__global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendArgs p,
+                                                          const int warps_per_tok) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);
+  const uint32_t ti = item / static_cast<uint32_t>(warps_per_tok);
+  if (ti >= static_cast<uint32_t>(p.tok)) return;
+  const int t = static_cast<int>(ti);
+  const int heads = p.hq + 2 * p.hkv;
+  constexpr int kPer = 32 / LG;  // heads of a step
+  const int j = lane % LG, sub = lane / LG;
+  const int first = static_cast<int>(item - ti * warps_per_tok) * STEPS * kPer;  // of the warp
+  const bool in = j < p.D / 16;
+  const bool rot = INTER ? 16 * j < p.R : j < p.R / 16;
+  // the lane's two pieces
+  const int ea = INTER || !rot ? 16 * j : 8 * j;
+  const int eb = INTER || !rot ? 16 * j + 8 : 8 * j + p.R / 2;
+
+  const uint16_t* row = p.qkv + t * p.ld_qkv;
+  auto source = [&](int hd) {
+    // q, k and v need not be neighbours in the row
+    const int kv = hd - p.hq;
+    const int at = kv < 0 ? p.off_q + hd * p.D
+                          : (kv < p.hkv ? p.off_k + kv * p.D : p.off_v + (kv - p.hkv) * p.D);
+    return row + at;
+  };
+  uint4 a[STEPS], b[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int hd = first + s * kPer + sub;
+    a[s] = b[s] = make_uint4(0, 0, 0, 0);
+    if (in && hd < heads) {
+      const uint16_t* src = source(hd);
+      a[s] = *reinterpret_cast<const uint4*>(src + ea);
+      b[s] = *reinterpret_cast<const uint4*>(src + eb);
+    }
+  }
+
+  // cosines and sines of frequencies 8j .. 8j+7, unless the warp has v only
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+  const int half = p.R / 2;
+  if (rot && first < p.hq + p.hkv) {
+    const uint32_t map = p.axis_of[j];
+    int64_t pos[kRopeMaxAxes];
+#pragma unroll
+    for (int x = 0; x < kRopeMaxAxes; ++x) pos[x] = x < p.axes ? rope_position(p, x, t) : 0;
+    if (8 * j + 8 <= half && (map == 0x0000u || map == 0x5555u || map == 0xAAAAu || map == 0xFFFFu)) {
+      const float* c = p.cos_sin + pos[0] * p.R;
+#pragma unroll
+      for (int x = 1; x < kRopeMaxAxes; ++x)
+        if ((map & 3u) == x) c = p.cos_sin + pos[x] * p.R;
+      c += 8 * j;
+      if ((reinterpret_cast<uintptr_t>(p.cos_sin) & 15) == 0 && half % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 u = __ldg(reinterpret_cast<const float4*>(c + i));
+          const float4 v = __ldg(reinterpret_cast<const float4*>(c + half + i));
+          cs[i] = u.x; cs[i + 1] = u.y; cs[i + 2] = u.z; cs[i + 3] = u.w;
+          sn[i] = v.x; sn[i + 1] = v.y; sn[i + 2] = v.z; sn[i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cs[i] = __ldg(c + i);
+          sn[i] = __ldg(c + half + i);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (8 * j + i >= half) break;
+        const uint32_t x = (map >> (2 * i)) & 3u;
+        const int64_t ps = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
+        const float* c = p.cos_sin + ps * p.R + 8 * j + i;
+        cs[i] = __ldg(c);
+        sn[i] = __ldg(c + half);
+      }
+    }
+  }
+
+  // the token's cache entry
+  int64_t k_at = 0, v_at = 0;
+  bool entry = false;
+  if (first + STEPS * kPer > p.hq) {
+    const int64_t slot = rope_index(p.slots, t, p.idx64);
+    entry = slot >= 0 && slot < p.pages * p.page_size;
+    if (entry) {
+      int64_t pg, at;
+      if (slot <= 0x7FFFFFFF) {
+        pg = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
+        at = static_cast<uint32_t>(slot) % static_cast<uint32_t>(p.page_size);
+      } else {
+        pg = slot / p.page_size;
+        at = slot % p.page_size;
+      }
+      k_at = pg * p.k_page + at * p.k_slot;
+      v_at = pg * p.v_page + at * p.v_slot;
+    }
+  }
+
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int h0 = first + s * kPer + sub;
+    const int kind = h0 < p.hq ? 0 : (h0 < p.hq + p.hkv ? 1 : 2);
+    float fa[8], fb[8];
+    rope_unpack<E>(a[s], fa);
+    rope_unpack<E>(b[s], fb);
+    if (NORM) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sum));
+      if (!in) sum = 0.f;
+#pragma unroll
+      for (int d = LG / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (kind < 2 && in) {
+        const float rstd = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+        const uint16_t* w = kind == 0 ? p.qw : p.kw;
+        float wa[8], wb[8];
+        rope_unpack<E>(__ldg(reinterpret_cast<const uint4*>(w + ea)), wa);
+        rope_unpack<E>(__ldg(reinterpret_cast<const uint4*>(w + eb)), wb);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          fa[i] *= rstd * (wa[i] + p.w0);
+          fb[i] *= rstd * (wb[i] + p.w0);
+        }
+      }
+    }
+    if (!in || h0 >= heads) continue;
+    if (kind < 2 && rot) {
+      if (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // the lane's frequencies may end within its pieces
+          const float x = fa[2 * i], y = fa[2 * i + 1], u = fb[2 * i], v = fb[2 * i + 1];
+          if (8 * j + i < half) {
+            fa[2 * i] = x * cs[i] - y * sn[i];
+            fa[2 * i + 1] = y * cs[i] + x * sn[i];
+          }
+          if (8 * j + 4 + i < half) {
+            fb[2 * i] = u * cs[4 + i] - v * sn[4 + i];
+            fb[2 * i + 1] = v * cs[4 + i] + u * sn[4 + i];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = fa[i], y = fb[i];
+          fa[i] = x * cs[i] - y * sn[i];
+          fb[i] = y * cs[i] + x * sn[i];
+        }
+      }
+    }
+    if (kind == 0) {
+      uint16_t* o = p.q_out + t * p.ld_q + h0 * p.D;
+      stg128(o + ea, rope_pack<E>(fa));
+      stg128(o + eb, rope_pack<E>(fb));
+    } else if (entry) {
+      const float inv = kind == 1 ? p.k_inv : p.v_inv;
+      const int64_t at = kind == 1 ? k_at + (h0 - p.hq) * p.k_head
+                                   : v_at + (h0 - p.hq - p.hkv) * p.v_head;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        fa[i] *= inv;
+        fb[i] *= inv;
+      }
+      if (C8) {
+        uint8_t* o = static_cast<uint8_t*>(kind == 1 ? p.kc : p.vc) + at;
+        stg64(o + ea, make_uint2(f4_to_e4m3(fa[0], fa[1], fa[2], fa[3]),
+                                 f4_to_e4m3(fa[4], fa[5], fa[6], fa[7])));
+        stg64(o + eb, make_uint2(f4_to_e4m3(fb[0], fb[1], fb[2], fb[3]),
+                                 f4_to_e4m3(fb[4], fb[5], fb[6], fb[7])));
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(kind == 1 ? p.kc : p.vc) + at;
+        stg128(o + ea, rope_pack<E>(fa));
+        stg128(o + eb, rope_pack<E>(fb));
+      }
+    }
+  }
 }
 
 }  // namespace lora
