@@ -16,10 +16,6 @@
 #define LORA_W4_MV_TOKENS 16 // 4-bit projection: tokens up to which w4_mv runs
 #endif
 
-#ifndef LORA_ROPE_STEPS
-#define LORA_ROPE_STEPS 4
-#endif
-
 namespace {
 
 // Lets a kernel take up to `bytes` of dynamic shared memory, once for each
@@ -46,7 +42,10 @@ template <class E, int VPT, bool AL>
 void launch_rmsnorm(const lora::RmsNormArgs& a, int T, cudaStream_t st) {
   const int rows = std::max(1, 256 / T);
   const unsigned grid = static_cast<unsigned>((a.tok + rows - 1) / rows);
-  lora::rmsnorm_kernel<E, VPT, AL><<<grid, dim3(T, rows), 0, st>>>(a);
+  if (a.q)
+    lora::rmsnorm_kernel<E, VPT, AL, true><<<grid, dim3(T, rows), 0, st>>>(a);
+  else
+    lora::rmsnorm_kernel<E, VPT, AL, false><<<grid, dim3(T, rows), 0, st>>>(a);
 }
 
 template <class E, bool AL>
@@ -55,9 +54,14 @@ lora_status rmsnorm(lora::RmsNormArgs a, cudaStream_t st) {
   // length; the widest rows have no thread for it and are cut at their start
   a.follow = (a.H + 14) / 8 <= 8 * 1024;
   const int blocks = AL ? a.H / 8 : (a.H + (a.follow ? 14 : 7)) / 8;
-  // blocks of eight a thread
+  // Blocks of eight a thread.  Where the rows fill the SMs several times over,
+  // up to 256 threads a row: a row's two or three barriers then cost the least
+  // (8192 x 5120: 60 us with up to 256, 65 with 512, 80 with 1024 threads a
+  // row); below that more threads, for the latency of each (777 x 3583: 8.5 us
+  // with 512 against 9.4 with 256).
+  const int most = a.tok >= 148 * 8 ? 256 : a.tok >= 148 ? 512 : 1024;
   int vpt = 1;
-  while (vpt < 8 && (blocks + vpt - 1) / vpt > (a.tok >= 148 ? 256 : 1024)) vpt *= 2;
+  while (vpt < 8 && (blocks + vpt - 1) / vpt > most) vpt *= 2;
   const int T = round_up((blocks + vpt - 1) / vpt, 32);
   switch (vpt) {
     case 1: launch_rmsnorm<E, 1, AL>(a, T, st); break;
@@ -111,16 +115,17 @@ extern "C" lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* res
 
 namespace {
 
-template <class E, bool C8, bool INTER, bool NORM, int STEPS>
-void launch_rope(const lora::RopeAppendArgs& a, int lg, unsigned grid, int wpt, cudaStream_t st) {
+template <class E, bool C8, bool INTER, bool NORM, int DEPTH>
+void launch_rope(const lora::RopeAppendArgs& a, int lg, unsigned grid, int parts,
+                 int steps, cudaStream_t st) {
   if (lg == 4)
-    lora::rope_append_kernel<E, C8, INTER, NORM, 4, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+    lora::rope_append_kernel<E, C8, INTER, NORM, 4, DEPTH><<<grid, 256, 0, st>>>(a, parts, steps);
   else if (lg == 8)
-    lora::rope_append_kernel<E, C8, INTER, NORM, 8, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+    lora::rope_append_kernel<E, C8, INTER, NORM, 8, DEPTH><<<grid, 256, 0, st>>>(a, parts, steps);
   else if (lg == 16)
-    lora::rope_append_kernel<E, C8, INTER, NORM, 16, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+    lora::rope_append_kernel<E, C8, INTER, NORM, 16, DEPTH><<<grid, 256, 0, st>>>(a, parts, steps);
   else
-    lora::rope_append_kernel<E, C8, INTER, NORM, 32, STEPS><<<grid, 256, 0, st>>>(a, wpt);
+    lora::rope_append_kernel<E, C8, INTER, NORM, 32, DEPTH><<<grid, 256, 0, st>>>(a, parts, steps);
 }
 
 template <class E, bool C8, bool INTER, bool NORM>
@@ -128,14 +133,19 @@ lora_status rope_pieces(const lora::RopeAppendArgs& a, cudaStream_t st) {
   int lg = 4;
   while (lg < a.D / 16) lg *= 2;
   const int all = ((a.hq + 2 * a.hkv) * lg + 31) / 32;  // steps of a token
-  // Beyond two steps for each warp that an SM holds, a warp takes four.
-  const bool many = all > 1 && static_cast<int64_t>(a.tok) * all > 148 * 64 * 2;
-  const int wpt = many ? (all + LORA_ROPE_STEPS - 1) / LORA_ROPE_STEPS : all;
-  const int64_t grid = (static_cast<int64_t>(a.tok) * wpt + 7) / 8;
-  if (grid >= (int64_t(1) << 28)) return LORA_ERR_UNSUPPORTED;
+  // A warp a step as long as the SMs hold most of those warps at once; then as
+  // few warps to a token as still fill the SMs.
+  const int64_t warps = 148 * 24;
+  int parts = all;
+  if (static_cast<int64_t>(a.tok) * all > 2 * warps)
+    parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(all, 2 * warps / a.tok)));
+  const int steps = (all + parts - 1) / parts;
+  parts = (all + steps - 1) / steps;
+  const int64_t grid = (static_cast<int64_t>(a.tok) + 7) / 8 * parts;
+  if (grid >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
   const unsigned g = static_cast<unsigned>(grid);
-  if (many) launch_rope<E, C8, INTER, NORM, LORA_ROPE_STEPS>(a, lg, g, wpt, st);
-  else launch_rope<E, C8, INTER, NORM, 1>(a, lg, g, wpt, st);
+  if (steps > 1) launch_rope<E, C8, INTER, NORM, 2>(a, lg, g, parts, steps, st);
+  else launch_rope<E, C8, INTER, NORM, 1>(a, lg, g, parts, steps, st);
   return LORA_OK;
 }
 

@@ -47,15 +47,21 @@ __device__ __forceinline__ uint32_t f4_to_e4m3(float a, float b, float c, float 
   return lo | (hi << 16);
 }
 
-// Eight elements e0 .. e0+7 of a row (those in [0, H)), as one 16-byte load
-// where the block is whole and aligned.  Plain loads: the outputs may be
-// written over the inputs, element by element.
+// Eight elements e0 .. e0+7 of a row (those in [0, H)): one 16-byte load where
+// they are whole and aligned, the two 16-byte blocks that cover them where
+// they are whole.  Plain loads: the outputs may be written over the inputs,
+// element by element.
 template <bool AL>
 __device__ __forceinline__ uint4 norm_load8(const uint16_t* row, int e0, int H) {
   const uint16_t* p = row + e0;
   bool whole = AL;
-  if (!whole) whole = e0 >= 0 && e0 + 8 <= H && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+  if (!whole) whole = e0 >= 0 && e0 + 8 <= H && off == 0;
   if (whole) return *reinterpret_cast<const uint4*>(p);
+  if (e0 >= 0 && e0 + 8 <= H) {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+    return bytes_at(q[0], q[1], off);
+  }
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -84,8 +90,9 @@ __device__ __forceinline__ void norm_store8(uint16_t* row, int e0, int H, uint4 
 
 // blockDim = (threads of a row, rows of the block), the first a multiple of 32.
 // VPT: blocks of eight elements that a thread holds.  AL: every row of every
-// tensor is 16-byte aligned (q: 8-byte) and H is a multiple of 8.
-template <class E, int VPT, bool AL>
+// tensor is 16-byte aligned (q: 8-byte) and H is a multiple of 8.  QUANT: q is
+// given.
+template <class E, int VPT, bool AL, bool QUANT>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const RmsNormArgs p) {
   __shared__ float ssum[32];
   __shared__ uint32_t smax[32];
@@ -97,32 +104,36 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const RmsNormArgs p) {
   const uint16_t* x = p.x + t * p.ld_x;
   // blocks of eight start where x's row crosses 16-byte boundaries
   const int shift = AL || !p.follow ? 0 : static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 1) & 7);
-  float h[VPT][8];
+  // All loads before the first store, which they would have to wait for; the
+  // weights too where there are registers for them, behind the sum otherwise.
+  uint4 xv[VPT], rv[VPT], wv[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e0 = 8 * (j * T + tid) - shift;
+    xv[j] = rv[j] = wv[j] = make_uint4(0, 0, 0, 0);
+    if (live && e0 < p.H) {
+      xv[j] = norm_load8<AL>(x, e0, p.H);
+      if (p.res) rv[j] = norm_load8<AL>(p.res + t * p.ld_res, e0, p.H);
+      if (VPT <= 2) wv[j] = norm_load8<AL>(p.w, e0, p.H);
+    }
+  }
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int e0 = 8 * (j * T + tid) - shift;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (live && e0 < p.H) {
-      v = norm_load8<AL>(x, e0, p.H);
-      if (p.res) {
-        const uint4 r = norm_load8<AL>(p.res + t * p.ld_res, e0, p.H);
-        uint32_t* a = reinterpret_cast<uint32_t*>(&v);
-        const uint32_t* b = reinterpret_cast<const uint32_t*>(&r);
+    uint32_t* a = reinterpret_cast<uint32_t*>(&xv[j]);
+    const uint32_t* b = reinterpret_cast<const uint32_t*>(&rv[j]);
+    if (p.res) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = E::u32_to_f2(a[i]), g = E::u32_to_f2(b[i]);
-          a[i] = E::f2_to_u32(f.x + g.x, f.y + g.y);
-        }
-        norm_store8<AL>(p.res_out + t * p.ld_res_out, e0, p.H, v);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = E::u32_to_f2(a[i]), g = E::u32_to_f2(b[i]);
+        a[i] = E::f2_to_u32(f.x + g.x, f.y + g.y);
       }
+      if (live && e0 < p.H) norm_store8<AL>(p.res_out + t * p.ld_res_out, e0, p.H, xv[j]);
     }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = E::u32_to_f2(w[i]);
-      h[j][2 * i] = f.x;
-      h[j][2 * i + 1] = f.y;
+      const float2 f = E::u32_to_f2(a[i]);
       sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
     }
   }
@@ -137,28 +148,32 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const RmsNormArgs p) {
   const float rstd = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
 
   uint32_t top = 0;  // bits of max |v|; a NaN's bits are above an infinity's
+  float v[QUANT ? VPT : 1][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int e0 = 8 * (j * T + tid) - shift;
-    if (live && e0 < p.H) {
-      const uint4 wv = norm_load8<AL>(p.w, e0, p.H);
-      const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
-      uint4 o;
-      uint32_t* ov = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = E::u32_to_f2(w[i]);
-        const float a = h[j][2 * i] * rstd * (f.x + p.w0);
-        const float b = h[j][2 * i + 1] * rstd * (f.y + p.w0);
-        h[j][2 * i] = a;
-        h[j][2 * i + 1] = b;
-        top = max(top, max(__float_as_uint(fabsf(a)), __float_as_uint(fabsf(b))));
-        ov[i] = E::f2_to_u32(a, b);
-      }
-      if (p.out) norm_store8<AL>(p.out + t * p.ld_out, e0, p.H, o);
-    }
+    if (VPT > 2 && live && e0 < p.H) wv[j] = norm_load8<AL>(p.w, e0, p.H);
   }
-  if (!p.q) return;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int e0 = 8 * (j * T + tid) - shift;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&wv[j]);
+    uint32_t* hv = reinterpret_cast<uint32_t*>(&xv[j]);
+    const int jj = QUANT ? j : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = E::u32_to_f2(w[i]), g = E::u32_to_f2(hv[i]);
+      const float a = g.x * rstd * (f.x + p.w0);
+      const float b = g.y * rstd * (f.y + p.w0);
+      v[jj][2 * i] = a;
+      v[jj][2 * i + 1] = b;
+      if (QUANT && live && e0 + 2 * i < p.H && e0 + 2 * i + 1 >= 0)
+        top = max(top, max(__float_as_uint(fabsf(a)), __float_as_uint(fabsf(b))));
+      hv[i] = E::f2_to_u32(a, b);
+    }
+    if (p.out && live && e0 < p.H) norm_store8<AL>(p.out + t * p.ld_out, e0, p.H, xv[j]);
+  }
+  if (!QUANT) return;
   top = __reduce_max_sync(0xffffffffu, top);
   if (warps > 1) {
     if ((tid & 31) == 0) smax[w0 + (tid >> 5)] = top;
@@ -177,8 +192,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const RmsNormArgs p) {
     const int e0 = 8 * (j * T + tid) - shift;
     if (live && e0 < p.H) {
       uint2 b;
-      b.x = f4_to_e4m3(h[j][0] * inv, h[j][1] * inv, h[j][2] * inv, h[j][3] * inv);
-      b.y = f4_to_e4m3(h[j][4] * inv, h[j][5] * inv, h[j][6] * inv, h[j][7] * inv);
+      const float(&f)[8] = v[QUANT ? j : 0];
+      b.x = f4_to_e4m3(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+      b.y = f4_to_e4m3(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
       uint8_t* d = p.q + t * p.ld_q + e0;
       bool whole = AL;
       if (!whole) whole = e0 >= 0 && e0 + 8 <= p.H && (reinterpret_cast<uintptr_t>(d) & 7) == 0;

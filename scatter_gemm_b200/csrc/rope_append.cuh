@@ -142,64 +142,57 @@ __device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
 // each lane eight neighbouring frequencies, that is two 16-byte pieces of the
 // head, R/2 apart, or next to each other when interleaved or behind the
 // rotated part; so a pair never leaves its lane and a head's norm is a few
-// shuffles.  A warp takes 32 / LG heads of one token at a time, STEPS times,
-// all of its loads first: with many tokens that keeps enough bytes under way
-// and reads the token's cosines and sines once for STEPS steps.
-template <class E, bool C8, bool INTER, bool NORM, int LG, int STEPS>
-__global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendArgs p,
-                                                          const int warps_per_tok) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t item = blockIdx.x * 8u + (threadIdx.x >> 5);
-  const uint32_t ti = item / static_cast<uint32_t>(warps_per_tok);
-  if (ti >= static_cast<uint32_t>(p.tok)) return;
-  const int t = static_cast<int>(ti);
-  const int heads = p.hq + 2 * p.hkv;
+// shuffles.  A warp takes 32 / LG heads of one token at a time, `steps` times,
+// DEPTH steps' loads under way: with many tokens that reads the token's
+// cosines, sines and slot once for all of its heads.
+//
+// A block is eight tokens and the same heads of each, so that which slice a
+// head belongs to, and where, is the same arithmetic for all of its threads.
+template <class E, bool C8, bool INTER, bool NORM, int LG, int DEPTH>
+__global__ void __launch_bounds__(256, DEPTH == 1 ? 1 : NORM ? 3 : 4)
+rope_append_kernel(const RopeAppendArgs p, const int parts, const int steps) {
   constexpr int kPer = 32 / LG;  // heads of a step
+  const int lane = threadIdx.x & 31;
+  const uint32_t tb = blockIdx.x / static_cast<uint32_t>(parts);
+  const int first = static_cast<int>(blockIdx.x - tb * parts) * (DEPTH > 1 ? steps : 1) * kPer;
+  const int t = static_cast<int>(tb * 8u + (threadIdx.x >> 5));
+  if (t >= p.tok) return;
+  const int end = min(p.hq + 2 * p.hkv, first + (DEPTH > 1 ? steps : 1) * kPer);
   const int j = lane % LG, sub = lane / LG;
-  const int first = static_cast<int>(item - ti * warps_per_tok) * STEPS * kPer;  // of the warp
   const bool in = j < p.D / 16;
-  const bool rot = INTER ? 16 * j < p.R : j < p.R / 16;
+  const int half = p.R / 2;
+  const bool rot = 8 * j < half;
   // the lane's two pieces
   const int ea = INTER || !rot ? 16 * j : 8 * j;
-  const int eb = INTER || !rot ? 16 * j + 8 : 8 * j + p.R / 2;
+  const int eb = INTER || !rot ? 16 * j + 8 : 8 * j + half;
 
+  // head hd starts at column hd * D + (its slice's start less the heads before it)
+  const int base_q = p.off_q, base_k = p.off_k - p.hq * p.D,
+            base_v = p.off_v - (p.hq + p.hkv) * p.D;
   const uint16_t* row = p.qkv + t * p.ld_qkv;
-  auto source = [&](int hd) {
-    // q, k and v need not be neighbours in the row
-    const int kv = hd - p.hq;
-    const int at = kv < 0 ? p.off_q + hd * p.D
-                          : (kv < p.hkv ? p.off_k + kv * p.D : p.off_v + (kv - p.hkv) * p.D);
-    return row + at;
-  };
-  uint4 a[STEPS], b[STEPS];
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int hd = first + s * kPer + sub;
-    a[s] = b[s] = make_uint4(0, 0, 0, 0);
-    if (in && hd < heads) {
-      const uint16_t* src = source(hd);
-      a[s] = *reinterpret_cast<const uint4*>(src + ea);
-      b[s] = *reinterpret_cast<const uint4*>(src + eb);
+  uint4 a[DEPTH], b[DEPTH];
+  auto load = [&](int hd, uint4& x, uint4& y) {
+    if (in && hd < end) {
+      const uint16_t* src =
+          row + (hd * p.D + (hd < p.hq ? base_q : hd < p.hq + p.hkv ? base_k : base_v));
+      x = *reinterpret_cast<const uint4*>(src + ea);
+      y = *reinterpret_cast<const uint4*>(src + eb);
     }
+  };
+#pragma unroll
+  for (int s = 0; s < DEPTH; ++s) {
+    a[s] = b[s] = make_uint4(0, 0, 0, 0);
+    load(first + s * kPer + sub, a[s], b[s]);
   }
 
-  // cosines and sines of frequencies 8j .. 8j+7, unless the warp has v only
+  // cosines and sines of frequencies 8j .. 8j+7, unless the block has v only
   float cs[8], sn[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-  const int half = p.R / 2;
-  if (rot && first < p.hq + p.hkv) {
-    const uint32_t map = p.axis_of[j];
-    int64_t pos[kRopeMaxAxes];
-#pragma unroll
-    for (int x = 0; x < kRopeMaxAxes; ++x) pos[x] = x < p.axes ? rope_position(p, x, t) : 0;
-    if (8 * j + 8 <= half && (map == 0x0000u || map == 0x5555u || map == 0xAAAAu || map == 0xFFFFu)) {
-      const float* c = p.cos_sin + pos[0] * p.R;
-#pragma unroll
-      for (int x = 1; x < kRopeMaxAxes; ++x)
-        if ((map & 3u) == x) c = p.cos_sin + pos[x] * p.R;
-      c += 8 * j;
-      if ((reinterpret_cast<uintptr_t>(p.cos_sin) & 15) == 0 && half % 4 == 0) {
+  if (first < p.hq + p.hkv) {
+    if (p.axes == 1 && half % 8 == 0 && (reinterpret_cast<uintptr_t>(p.cos_sin) & 15) == 0) {
+      if (rot) {
+        const float* c = p.cos_sin + rope_position(p, 0, t) * p.R + 8 * j;
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
           const float4 u = __ldg(reinterpret_cast<const float4*>(c + i));
@@ -207,30 +200,40 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendArgs p
           cs[i] = u.x; cs[i + 1] = u.y; cs[i + 2] = u.z; cs[i + 3] = u.w;
           sn[i] = v.x; sn[i + 1] = v.y; sn[i + 2] = v.z; sn[i + 3] = v.w;
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cs[i] = __ldg(c + i);
-          sn[i] = __ldg(c + half + i);
-        }
       }
     } else {
+      // several axes, or a table or an end off the 16-byte grid: the warp
+      // gathers the token's row first, a frequency a lane, zeros behind it
+      __shared__ __align__(16) float rows[8][2][kRopeMaxDim / 2 + 8];
+      float(&tab)[2][kRopeMaxDim / 2 + 8] = rows[threadIdx.x >> 5];
+      for (int i = lane; i < (half + 7) / 8 * 8; i += 32) {
+        float u = 0.f, v = 0.f;
+        if (i < half) {
+          const int axis = (p.axis_of[i >> 3] >> (2 * (i & 7))) & 3;
+          const float* c = p.cos_sin + rope_position(p, axis, t) * p.R + i;
+          u = __ldg(c);
+          v = __ldg(c + half);
+        }
+        tab[0][i] = u;
+        tab[1][i] = v;
+      }
+      __syncwarp();
+      if (rot) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (8 * j + i >= half) break;
-        const uint32_t x = (map >> (2 * i)) & 3u;
-        const int64_t ps = x == 0 ? pos[0] : x == 1 ? pos[1] : x == 2 ? pos[2] : pos[3];
-        const float* c = p.cos_sin + ps * p.R + 8 * j + i;
-        cs[i] = __ldg(c);
-        sn[i] = __ldg(c + half);
+        for (int i = 0; i < 8; i += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(&tab[0][8 * j + i]);
+          const float4 v = *reinterpret_cast<const float4*>(&tab[1][8 * j + i]);
+          cs[i] = u.x; cs[i + 1] = u.y; cs[i + 2] = u.z; cs[i + 3] = u.w;
+          sn[i] = v.x; sn[i + 1] = v.y; sn[i + 2] = v.z; sn[i + 3] = v.w;
+        }
       }
     }
   }
 
-  // the token's cache entry
+  // the token's cache entry, less the heads before the slice
   int64_t k_at = 0, v_at = 0;
   bool entry = false;
-  if (first + STEPS * kPer > p.hq) {
+  if (end > p.hq) {
     const int64_t slot = rope_index(p.slots, t, p.idx64);
     entry = slot >= 0 && slot < p.pages * p.page_size;
     if (entry) {
@@ -242,87 +245,99 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendArgs p
         pg = slot / p.page_size;
         at = slot % p.page_size;
       }
-      k_at = pg * p.k_page + at * p.k_slot;
-      v_at = pg * p.v_page + at * p.v_slot;
+      k_at = pg * p.k_page + at * p.k_slot - p.hq * p.k_head;
+      v_at = pg * p.v_page + at * p.v_slot - (p.hq + p.hkv) * p.v_head;
     }
   }
 
+  uint16_t* q_row = p.q_out + t * p.ld_q;
+  for (int s0 = 0; s0 < (DEPTH > 1 ? steps : 1); s0 += DEPTH) {
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int h0 = first + s * kPer + sub;
-    const int kind = h0 < p.hq ? 0 : (h0 < p.hq + p.hkv ? 1 : 2);
-    float fa[8], fb[8];
-    rope_unpack<E>(a[s], fa);
-    rope_unpack<E>(b[s], fb);
-    if (NORM) {
-      float sum = 0.f;
+    for (int s = 0; s < DEPTH; ++s) {
+      if (first + (s0 + s) * kPer >= end) break;
+      const int hd = first + (s0 + s) * kPer + sub;
+      const bool is_q = hd < p.hq, is_k = !is_q && hd < p.hq + p.hkv, is_v = hd >= p.hq + p.hkv;
+      const float inv = is_q ? 1.f : is_k ? p.k_inv : p.v_inv;
+      uint4 oa = a[s], ob = b[s];
+      if (DEPTH > 1) load(hd + DEPTH * kPer, a[s], b[s]);
+      // v, and pieces behind the rotated part, pass through as they are
+      float fa[8], fb[8];
+      rope_unpack<E>(oa, fa);
+      rope_unpack<E>(ob, fb);
+      if (NORM) {
+        float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sum));
-      if (!in) sum = 0.f;
+        for (int i = 0; i < 8; ++i) sum = fmaf(fa[i], fa[i], fmaf(fb[i], fb[i], sum));
 #pragma unroll
-      for (int d = LG / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (kind < 2 && in) {
-        const float rstd = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-        const uint16_t* w = kind == 0 ? p.qw : p.kw;
-        float wa[8], wb[8];
-        rope_unpack<E>(__ldg(reinterpret_cast<const uint4*>(w + ea)), wa);
-        rope_unpack<E>(__ldg(reinterpret_cast<const uint4*>(w + eb)), wb);
+        for (int d = LG / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (!is_v && in) {
+          const float rstd = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
+          const uint16_t* w = is_q ? p.qw : p.kw;
+          float wa[8], wb[8];
+          rope_unpack<E>(__ldg(reinterpret_cast<const uint4*>(w + ea)), wa);
+          rope_unpack<E>(__ldg(reinterpret_cast<const uint4*>(w + eb)), wb);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          fa[i] *= rstd * (wa[i] + p.w0);
-          fb[i] *= rstd * (wb[i] + p.w0);
-        }
-      }
-    }
-    if (!in || h0 >= heads) continue;
-    if (kind < 2 && rot) {
-      if (INTER) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // the lane's frequencies may end within its pieces
-          const float x = fa[2 * i], y = fa[2 * i + 1], u = fb[2 * i], v = fb[2 * i + 1];
-          if (8 * j + i < half) {
-            fa[2 * i] = x * cs[i] - y * sn[i];
-            fa[2 * i + 1] = y * cs[i] + x * sn[i];
-          }
-          if (8 * j + 4 + i < half) {
-            fb[2 * i] = u * cs[4 + i] - v * sn[4 + i];
-            fb[2 * i + 1] = v * cs[4 + i] + u * sn[4 + i];
+          for (int i = 0; i < 8; ++i) {
+            fa[i] *= rstd * (wa[i] + p.w0);
+            fb[i] *= rstd * (wb[i] + p.w0);
           }
         }
-      } else {
+      }
+      if (!in || hd >= end || (!is_q && !entry)) continue;
+      if (!is_v && rot) {
+        if (INTER) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = fa[i], y = fb[i];
-          fa[i] = x * cs[i] - y * sn[i];
-          fb[i] = y * cs[i] + x * sn[i];
+          for (int i = 0; i < 4; ++i) {
+            // the lane's frequencies may end within its pieces
+            const float x = fa[2 * i], y = fa[2 * i + 1], u = fb[2 * i], v = fb[2 * i + 1];
+            if (8 * j + i < half) {
+              fa[2 * i] = x * cs[i] - y * sn[i];
+              fa[2 * i + 1] = y * cs[i] + x * sn[i];
+            }
+            if (8 * j + 4 + i < half) {
+              fb[2 * i] = u * cs[4 + i] - v * sn[4 + i];
+              fb[2 * i + 1] = v * cs[4 + i] + u * sn[4 + i];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x = fa[i], y = fb[i];
+            fa[i] = x * cs[i] - y * sn[i];
+            fb[i] = y * cs[i] + x * sn[i];
+          }
         }
       }
-    }
-    if (kind == 0) {
-      uint16_t* o = p.q_out + t * p.ld_q + h0 * p.D;
-      stg128(o + ea, rope_pack<E>(fa));
-      stg128(o + eb, rope_pack<E>(fb));
-    } else if (entry) {
-      const float inv = kind == 1 ? p.k_inv : p.v_inv;
-      const int64_t at = kind == 1 ? k_at + (h0 - p.hq) * p.k_head
-                                   : v_at + (h0 - p.hq - p.hkv) * p.v_head;
+      if (C8 && !is_q) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        fa[i] *= inv;
-        fb[i] *= inv;
-      }
-      if (C8) {
-        uint8_t* o = static_cast<uint8_t*>(kind == 1 ? p.kc : p.vc) + at;
+        for (int i = 0; i < 8; ++i) {
+          fa[i] *= inv;
+          fb[i] *= inv;
+        }
+        uint8_t* o = static_cast<uint8_t*>(is_k ? p.kc : p.vc) +
+                     (is_k ? k_at + hd * p.k_head : v_at + hd * p.v_head);
         stg64(o + ea, make_uint2(f4_to_e4m3(fa[0], fa[1], fa[2], fa[3]),
                                  f4_to_e4m3(fa[4], fa[5], fa[6], fa[7])));
         stg64(o + eb, make_uint2(f4_to_e4m3(fb[0], fb[1], fb[2], fb[3]),
                                  f4_to_e4m3(fb[4], fb[5], fb[6], fb[7])));
-      } else {
-        uint16_t* o = static_cast<uint16_t*>(kind == 1 ? p.kc : p.vc) + at;
-        stg128(o + ea, rope_pack<E>(fa));
-        stg128(o + eb, rope_pack<E>(fb));
+        continue;
       }
+      if (inv != 1.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          fa[i] *= inv;
+          fb[i] *= inv;
+        }
+      }
+      if (!is_v || inv != 1.f) {
+        oa = rope_pack<E>(fa);
+        ob = rope_pack<E>(fb);
+      }
+      uint16_t* o = is_q ? q_row + hd * p.D
+                         : static_cast<uint16_t*>(is_k ? p.kc : p.vc) +
+                               (is_k ? k_at + hd * p.k_head : v_at + hd * p.v_head);
+      stg128(o + ea, oa);
+      stg128(o + eb, ob);
     }
   }
 }
