@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -421,12 +422,13 @@ def lora_base_expand(x: torch.Tensor, W: torch.Tensor, in_r: torch.Tensor,
 _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, tok: int, width: int, device) -> int:
-    """Checks a [tok, >= width] tensor of unit inner stride; returns its row stride."""
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, tok: int, width: int, dev: int) -> int:
+    """Checks a [tok, >= width] tensor of unit inner stride on device `dev`;
+    returns its row stride."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors, got {t.device}")
     if t.dim() != 2 or t.shape[0] != tok or t.shape[1] < width:
         raise ValueError(f"{name} must be [{tok}, >= {width}], got {tuple(t.shape)}")
     ld, inner = t.stride()
@@ -439,28 +441,39 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, tok: int, width: int, 
     return ld
 
 
-def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, device) -> int:
+def _ld(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> int:
+    """_rows for a tensor that should have exactly `shape`: the usual case in
+    few steps, as these calls' time on the host is that of a small launch."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        ld, inner = t.stride()
+        if inner == 1 and ld >= shape[1]:
+            return ld
+    return _rows(t, name, dtype, shape[0], shape[1], dev)
+
+
+def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
     """Checks a contiguous 1-D tensor of n elements; returns its address."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{n}] tensor on {device}")
+    if t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor on the others' device")
     return t.data_ptr()
 
 
-def _call_on(device: torch.device, name: str, fn, args, stream) -> None:
+def _call_on(dev: int, name: str, args, stream) -> None:
     """Calls an entry point with the tensors' device current, on the given
     stream or that device's current one."""
-    if device.type != "cuda":
-        raise ValueError(f"{name} needs CUDA tensors, got {device}")
+    if dev < 0:
+        raise ValueError(f"{name} needs CUDA tensors")
+    fn = getattr(_lib or lib(), name)
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
         raw = _stream(stream)
-    if device.index == torch._C._cuda_getDevice():
+    if dev == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             st = fn(*args, raw)
     if st != LORA_OK:
         raise LoraError(name, st)
@@ -479,34 +492,34 @@ def lora_rmsnorm(x: torch.Tensor, weight: torch.Tensor, out: Optional[torch.Tens
     the 8-bit form, out = out_q * out_scale[:, None] within rounding; `out` may
     then be None.  Returns out, or out_q where out is None."""
     dt = _dtype_code(x)
-    if x.dim() != 2:
-        raise ValueError(f"x must be 2-D, got {tuple(x.shape)}")
-    tok, H = x.shape
-    dtype, dev = x.dtype, x.device
-    ld_x = _rows(x, "x", dtype, tok, H, dev)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be 2-D, got {tuple(shape)}")
+    tok, H = shape
+    dtype, dev = x.dtype, x.get_device()
+    ld_x = _ld(x, "x", dtype, shape, dev)
     w = _flat(weight, "weight", dtype, H, dev)
     ptr_r = ptr_ro = ptr_o = ptr_q = ptr_s = None
     ld_r = ld_ro = ld_o = ld_q = 0
     if residual is not None:
-        ld_r, ptr_r = _rows(residual, "residual", dtype, tok, H, dev), residual.data_ptr()
-        ld_ro, ptr_ro = ld_r, ptr_r
+        ld_ro = ld_r = _ld(residual, "residual", dtype, shape, dev)
+        ptr_ro = ptr_r = residual.data_ptr()
     if residual_out is not None:
         if residual is None:
             raise ValueError("residual_out needs a residual")
-        ld_ro = _rows(residual_out, "residual_out", dtype, tok, H, dev)
+        ld_ro = _ld(residual_out, "residual_out", dtype, shape, dev)
         ptr_ro = residual_out.data_ptr()
     if out is not None:
-        ld_o, ptr_o = _rows(out, "out", dtype, tok, H, dev), out.data_ptr()
+        ld_o, ptr_o = _ld(out, "out", dtype, shape, dev), out.data_ptr()
     if (out_q is None) != (out_scale is None):
         raise ValueError("out_q and out_scale go together")
     if out_q is not None:
-        ld_q = _rows(out_q, "out_q", torch.float8_e4m3fn, tok, H, dev)
-        ptr_q = out_q.data_ptr()
+        ld_q, ptr_q = _ld(out_q, "out_q", torch.float8_e4m3fn, shape, dev), out_q.data_ptr()
         ptr_s = _flat(out_scale, "out_scale", torch.float32, tok, dev)
     elif out is None:
         raise ValueError("out or out_q is required")
     if tok:
-        _call_on(dev, "lora_rmsnorm", lib().lora_rmsnorm,
+        _call_on(dev, "lora_rmsnorm",
                  (x.data_ptr(), ld_x, ptr_r, ld_r, ptr_ro, ld_ro, w, weight_offset, eps, ptr_o,
                   ld_o, ptr_q, ld_q, ptr_s, tok, H, dt), stream)
     return out if out is not None else out_q
@@ -525,38 +538,39 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     type; w_zeros uint8 of the same shape (default: 8 everywhere); out [tok,
     >= N] is written in its first N columns."""
     dt = _dtype_code(out)
-    if x.dim() != 2 or w_packed.dim() != 2:
+    x_shape, w_shape = x.shape, w_packed.shape
+    if len(x_shape) != 2 or len(w_shape) != 2:
         raise ValueError("x and w_packed must be 2-D")
-    tok, K = x.shape
-    N = w_packed.shape[0]
-    dev = x.device
-    x_dt = _CODES.get(x.dtype, -1)
+    tok, K = x_shape
+    N = w_shape[0]
+    dtype, x_dtype, dev = out.dtype, x.dtype, x.get_device()
+    x_dt = _CODES.get(x_dtype, -1)
     if x_dt != 2 and x_dt != dt:
-        raise TypeError(f"x must be {out.dtype} or float8_e4m3fn, got {x.dtype}")
+        raise TypeError(f"x must be {dtype} or float8_e4m3fn, got {x_dtype}")
     if group_size not in (32, 64, 128):
         raise ValueError("group_size must be 32, 64 or 128")
     if K < 1:
         raise ValueError("x must have at least one column")
-    G = -(-K // group_size)
-    ld_x = _rows(x, "x", x.dtype, tok, K, dev)
+    s_shape = (-(-K // group_size), N)
+    ld_x = _ld(x, "x", x_dtype, x_shape, dev)
     ld_w = _rows(w_packed, "w_packed", torch.uint8, N, -(-K // 32) * 16, dev)
     if N == 1:  # a single row of any stride, packed in whole 16-byte blocks
         ld_w = -(-K // 32) * 16
-    ld_s = _rows(w_scales, "w_scales", out.dtype, G, N, dev)
-    if w_scales.shape[1] != N:
-        raise ValueError(f"w_scales must be [{G}, {N}], got {tuple(w_scales.shape)}")
+    ld_s = _ld(w_scales, "w_scales", dtype, s_shape, dev)
+    if w_scales.shape != s_shape:
+        raise ValueError(f"w_scales must be {s_shape}, got {tuple(w_scales.shape)}")
     ptr_z = ptr_sx = None
     if w_zeros is not None:
-        if _rows(w_zeros, "w_zeros", torch.uint8, G, N, dev) != ld_s or w_zeros.shape[1] != N:
+        if _ld(w_zeros, "w_zeros", torch.uint8, s_shape, dev) != ld_s or w_zeros.shape != s_shape:
             raise ValueError("w_zeros must have the shape and row stride of w_scales")
         ptr_z = w_zeros.data_ptr()
     if (x_scale is not None) != (x_dt == 2):
         raise ValueError("x_scale goes with an 8-bit x")
     if x_scale is not None:
         ptr_sx = _flat(x_scale, "x_scale", torch.float32, tok, dev)
-    ld_o = _rows(out, "out", out.dtype, tok, N, dev)
+    ld_o = _ld(out, "out", dtype, (tok, N), dev)
     if tok and N:
-        _call_on(dev, "lora_w4_project", lib().lora_w4_project,
+        _call_on(dev, "lora_w4_project",
                  (x.data_ptr(), ld_x, ptr_sx, w_packed.data_ptr(), ld_w, w_scales.data_ptr(),
                   ptr_z, ld_s, out.data_ptr(), ld_o, tok, K, N, group_size, x_dt, dt), stream)
     return out
@@ -637,16 +651,21 @@ def rope_axis_map(sections: Sequence[int], interleaved: bool = False) -> list:
     return [i % m if i < m * sec[i % m] else 0 for i in range(sum(sec))]
 
 
-def _cache(t: torch.Tensor, name: str, hkv: int, D: int, device):
-    """Checks a [pages, page_size, Hkv, D] cache of any strides but the last."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 4 or t.shape[2] != hkv or t.shape[3] != D:
-        raise ValueError(f"{name} must be [pages, page_size, {hkv}, {D}], got {tuple(t.shape)}")
-    st = t.stride()
-    if st[3] != 1 and D > 1:
+_PACK4, _PACK3 = struct.Struct("=4i").pack, struct.Struct("=3q").pack
+
+
+def _cache(t: torch.Tensor, name: str, hkv: int, D: int, dev: int) -> bytes:
+    """Checks a [pages, page_size, Hkv, D] cache of any strides but the last;
+    returns the others as C integers."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors, got {t.device}")
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != hkv or shape[3] != D:
+        raise ValueError(f"{name} must be [pages, page_size, {hkv}, {D}], got {tuple(shape)}")
+    page, slot, head, inner = t.stride()
+    if inner != 1 and D > 1:
         raise ValueError(f"{name} must have a unit inner stride")
-    return (ctypes.c_int64 * 3)(st[0], st[1], st[2])
+    return _PACK3(page, slot, head)
 
 
 def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: int,
@@ -672,67 +691,72 @@ def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: 
     and k_weight [head_dim] normalise each head first.  q_out [tok, Hq *
     head_dim] defaults to the q slice itself, in place."""
     dt = _dtype_code(qkv)
-    if qkv.dim() != 2:
-        raise ValueError(f"qkv must be 2-D, got {tuple(qkv.shape)}")
+    shape = qkv.shape
+    if len(shape) != 2:
+        raise ValueError(f"qkv must be 2-D, got {tuple(shape)}")
     if len(slice_offsets) != 4:
         raise ValueError("slice_offsets needs 4 entries")
     o0, o1, o2, o3 = slice_offsets
-    tok, dev, D = qkv.shape[0], qkv.device, head_dim
+    dtype, tok, dev, D = qkv.dtype, shape[0], qkv.get_device(), head_dim
     if not 0 <= o0 <= o1 <= o2 <= o3 or D < 1 or (o1 - o0) % D or (o2 - o1) % D or \
             o3 - o2 != o2 - o1:
         raise ValueError("slice_offsets must span whole heads, as many of k as of v")
-    ld = _rows(qkv, "qkv", qkv.dtype, tok, o3, dev)
+    if o3 > shape[1]:
+        raise ValueError(f"qkv must have at least {o3} columns, got {shape[1]}")
+    ld = _ld(qkv, "qkv", dtype, shape, dev)
     idt = slots.dtype
-    if idt not in (torch.int32, torch.int64) or positions.dtype != idt:
-        raise TypeError("positions and slots must both be int32 or both int64")
+    if idt not in (torch.int32, torch.int64) or positions.dtype is not idt:
+        raise TypeError("positions and slots must both be int32 or both be int64")
     ptr_s = _flat(slots, "slots", idt, tok, dev)
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or \
-            cos_sin.device != dev:
-        raise ValueError(f"cos_sin must be a contiguous fp32 [max_pos, R] tensor on {dev}")
-    max_pos, R = cos_sin.shape
+    table = cos_sin.shape
+    if len(table) != 2 or cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous() or \
+            cos_sin.get_device() != dev:
+        raise ValueError("cos_sin must be a contiguous fp32 [max_pos, R] tensor on qkv's device")
+    max_pos, R = table
     if R > D or R % 2 or (R and max_pos < 1):
         raise ValueError("cos_sin must have 2 * frequencies <= head_dim columns and a row")
+    axes, ld_pos, amap = 1, 0, None
     if positions.dim() == 1:
-        axes, ld_pos = 1, 0
-        _flat(positions, "positions", idt, tok, dev)
+        ptr_p = _flat(positions, "positions", idt, tok, dev)
         if axis_map is not None:
             raise ValueError("axis_map needs positions of [axes, tok]")
-        amap = None
     else:
         axes = positions.shape[0]
         ld_pos = _rows(positions, "positions", idt, axes, tok, dev)
+        ptr_p = positions.data_ptr()
         if positions.shape[1] != tok or not 1 <= axes <= 4:
             raise ValueError(f"positions must be [tok] or [1..4, {tok}]")
-        if axis_map is None and axes > 1:
+        if axis_map is not None:
+            amap = bytes(axis_map)
+            if len(amap) != R // 2 or (amap and max(amap) >= axes):
+                raise ValueError(f"axis_map needs {R // 2} axis numbers below {axes}")
+        elif axes > 1:
             raise ValueError("positions of several axes need an axis_map")
-        amap = bytes(axis_map) if axis_map is not None else None
-        if amap is not None and (len(amap) != R // 2 or (amap and max(amap) >= axes)):
-            raise ValueError(f"axis_map needs {R // 2} axis numbers below {axes}")
     hkv = (o2 - o1) // D
     ks = _cache(k_cache, "k_cache", hkv, D, dev)
     vs = _cache(v_cache, "v_cache", hkv, D, dev)
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    c_shape, c_dtype = k_cache.shape, k_cache.dtype
+    if c_shape != v_cache.shape or c_dtype is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must share shape and element type")
-    c_dt = _CODES.get(k_cache.dtype, -1)
+    c_dt = _CODES.get(c_dtype, -1)
     if c_dt != dt and c_dt != 2:
-        raise TypeError(f"the caches must be {qkv.dtype} or float8_e4m3fn, got {k_cache.dtype}")
+        raise TypeError(f"the caches must be {dtype} or float8_e4m3fn, got {c_dtype}")
     if q_out is None:
         q_out = qkv[:, o0:o1]
-    ld_q = _rows(q_out, "q_out", qkv.dtype, tok, o1 - o0, dev)
+    ld_q = _ld(q_out, "q_out", dtype, (tok, o1 - o0), dev)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     qw = kw = None
     if q_weight is not None:
-        qw = _flat(q_weight, "q_weight", qkv.dtype, D, dev)
-        kw = _flat(k_weight, "k_weight", qkv.dtype, D, dev)
+        qw = _flat(q_weight, "q_weight", dtype, D, dev)
+        kw = _flat(k_weight, "k_weight", dtype, D, dev)
     if tok:
-        _call_on(dev, "lora_rope_append", lib().lora_rope_append,
-                 (qkv.data_ptr(), ld, (ctypes.c_int32 * 4)(o0, o1, o2, o3), D, R,
-                  positions.data_ptr(), ld_pos, axes, amap, cos_sin.data_ptr(), max_pos,
-                  int(interleaved), qw, kw, weight_offset, eps, q_out.data_ptr(), ld_q,
-                  k_cache.data_ptr(), ks, v_cache.data_ptr(), vs,
-                  k_cache.shape[0] if k_cache.shape[1] else 0, max(k_cache.shape[1], 1), c_dt, k_scale, v_scale, ptr_s, idt.itemsize, tok, dt),
-                 stream)
+        _call_on(dev, "lora_rope_append",
+                 (qkv.data_ptr(), ld, _PACK4(o0, o1, o2, o3), D, R, ptr_p, ld_pos, axes, amap,
+                  cos_sin.data_ptr(), max_pos, interleaved, qw, kw, weight_offset, eps,
+                  q_out.data_ptr(), ld_q, k_cache.data_ptr(), ks, v_cache.data_ptr(), vs,
+                  c_shape[0] if c_shape[1] else 0, c_shape[1] or 1, c_dt, k_scale, v_scale,
+                  ptr_s, 8 if idt is torch.int64 else 4, tok, dt), stream)
     return q_out
 
 
