@@ -20,11 +20,17 @@ namespace {
 
 // Lets a kernel take up to `bytes` of dynamic shared memory, once for each
 // device (`ready` holds a bit for each).
-bool set_smem_once(std::atomic<uint64_t>& ready, const void* kernel, int bytes) {
+// A kernel whose warps pass registers among themselves must have been compiled
+// to at least `regs` registers a thread, or a warp could wait for more than
+// the block has.
+bool set_smem_once(std::atomic<uint64_t>& ready, const void* kernel, int bytes, int regs = 0) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
   const uint64_t bit = uint64_t(1) << dev;
   if (ready.load(std::memory_order_acquire) & bit) return true;
+  cudaFuncAttributes attr;
+  if (regs && (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess || attr.numRegs < regs))
+    return false;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
       cudaSuccess)
     return false;
@@ -350,7 +356,9 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
     return LORA_ERR_CUDA;
   auto kernel = lora::w4_tc_kernel<E, X8, NT, GS, SETS, SW>;
   static std::atomic<uint64_t> ready{0};  // a bit for each device
-  if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem)) return LORA_ERR_CUDA;
+  if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem,
+                     C::kSplit ? C::kRegs : 0))
+    return LORA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(P.cs > 1 ? tiles * P.cs : std::min<int64_t>(tiles, sms)));
   cfg.blockDim = dim3(C::kThreads);
@@ -375,7 +383,7 @@ lora_status w4_project_group(const lora::W4Args& a, int sms, cudaStream_t st) {
   if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4, 4>(a, sms, st);
   if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4, 4>(a, sms, st);
   if (a.tok <= 64) return w4_tc<E, X8, 64, GS, 4, 8>(a, sms, st);
-  return w4_tc<E, X8, 128, GS, 2, 8>(a, sms, st);
+  return w4_tc<E, X8, 128, GS, 4, 8>(a, sms, st);
 }
 
 template <class E, bool X8>

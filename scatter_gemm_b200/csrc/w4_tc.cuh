@@ -129,6 +129,67 @@ struct RingPos {
   }
 };
 
+// Two fp32 values in a 64-bit register, for the fused multiply-add of pairs:
+// c = a * s + c in each half, each rounded as one fma.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(s));
+}
+
+// Loads that stay where they are written: the compiler may move an ordinary
+// load of constant data down to its use, and the prefetch is gone.
+__device__ __forceinline__ uint32_t ld_early(const uint16_t* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_early(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+
+// mbar_wait for a role that waits much of its time: the hardware holds the
+// warp back for up to 20 us a try, so that it does not take issue slots from
+// the roles that it waits for.  Gives up after 1 s like every wait.
+__device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
+      record_error(kErrWaitTimeout);
+      return false;
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
@@ -136,12 +197,14 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // NT: tokens of a tile.  GS: log2 of the group size.  SETS: sets of four
-// widening warps.  SW: scaling warps, four, or eight that split the tokens.
+// widening warps.  SW: scaling warps, four, or eight that
+// split the tokens.
 template <bool X8, int NT, int GS, int SETS, int SW>
 struct W4Tc {
   static constexpr int kWide = 4 * SETS;                        // widening warps
   static constexpr int kTmaWarp = kWide + SW, kMmaWarp = kTmaWarp + 1;
-  static constexpr int kThreads = 32 * (kWide + SW + 3);
+  // the fourth of the last four warps only makes them a warpgroup
+  static constexpr int kThreads = 32 * (kWide + SW + 4);
   static constexpr int kGroups = 128 >> GS;                     // groups of a block
   static constexpr int kACols = X8 ? 32 : 64;                   // TMEM columns of a widened block
   static constexpr int kTmem = 512;
@@ -158,6 +221,15 @@ struct W4Tc {
   static constexpr int kStage = kWBytes + kXBytes;
   static constexpr int kCols = NT / (SW / 4);                   // tokens of a scaling warp
   static constexpr int kMmaArrive = kGroups > 1 ? 2 : 1;        // MMA warps that share a block
+  // With 64 sums a thread, the scaling warps take registers over from the
+  // others (setmaxnreg, by warpgroups): the three shares are at most what the
+  // block is launched with, kRegs for each thread.
+  static constexpr bool kSplit = kCols > 32;
+  static constexpr int kRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegsWide = 64, kRegsRest = 40, kRegsScale = 104;
+  static_assert(!kSplit || kWide * kRegsWide + SW * kRegsScale + 4 * kRegsRest <=
+                               (kWide + SW + 4) * kRegs,
+                "more registers than the block has");
   static_assert(kABufs >= kRing, "a widened block for each set");
 };
 
@@ -226,6 +298,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
 
   if (warp < C::kWide) {
     // =========================== widening: a lane of TMEM, and a row, a thread
+    if constexpr (C::kSplit) regs_dec<C::kRegsWide>();
     const int quad = warp & 3, set = warp >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
@@ -239,38 +312,40 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     int skip = set;  // blocks of the next tile before this set's first
     for (int tile = first; tile < tiles && ok; tile += step) {
       const int n = (tile % P.tiles_n) * kW4M + row;
-      const bool zin = p.z != nullptr && n < p.N;
-      // the zero points of a block, some blocks ahead.  They stay as loaded,
-      // each in a register of its own: arithmetic on a value that is on its
-      // way, even moving it, would wait for it.
-      constexpr int kAhead = SETS > 2 ? 2 : 4;
-      uint32_t zq[kAhead][C::kGroups];
-      auto zeros = [&](int kb, uint32_t (&v)[C::kGroups]) {
+      const uint8_t* z_row = p.z + min(n, p.N - 1);
+      const int last_g = (p.K - 1) >> GS;
+      // The zero points of this set's next kAhead blocks, loaded while it
+      // works on the last kAhead, and used as loaded: arithmetic on a value
+      // that is on its way, even moving it, would wait for it.
+      constexpr int kAhead = 2;
+      uint32_t zq[kAhead][C::kGroups], zn[kAhead][C::kGroups];
+      auto zeros = [&](int kb, uint32_t (&v)[kAhead][C::kGroups]) {
 #pragma unroll
-        for (int i = 0; i < C::kGroups; ++i) {
-          const int gi = kb * C::kGroups + i;
-          if (zin && kb < kb1 && (gi << GS) < p.K) v[i] = __ldg(p.z + gi * p.ld_s + n);
-        }
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int i = 0; i < C::kGroups; ++i)
+            v[u][i] = p.z ? ld_early(z_row + min((kb + u * SETS) * C::kGroups + i, last_g) * p.ld_s)
+                          : 8u;
       };
       int kb = kb0 + skip;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-        for (int i = 0; i < C::kGroups; ++i) zq[u][i] = 8;
-        zeros(kb + u * SETS, zq[u]);
-      }
+      zeros(kb, zn);
       while (kb < kb1 && ok) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+          for (int i = 0; i < C::kGroups; ++i) zq[u][i] = zn[u][i];
+        zeros(kb + kAhead * SETS, zn);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           if (kb >= kb1 || !ok) break;
-          ok = mbar_wait(full0 + 8 * st.i, st.fill());
+          ok = role_wait(full0 + 8 * st.i, st.fill());
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint8_t* src = smem + st.i * C::kStage + row * 64;
           uint4 pk[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) pk[c] = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
-          ok = mbar_wait(aempty0 + 8 * ab.i, ab.drain());
+          ok = role_wait(aempty0 + 8 * ab.i, ab.drain());
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -303,7 +378,6 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
               tmem_st16(dst + c * 16, r);
             }
           }
-          zeros(kb + kAhead * SETS, zq[u]);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -323,6 +397,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     }
   } else if (warp < C::kTmaWarp) {
     // =========================== scaling: sum += scale * accumulator, then the output
+    if constexpr (C::kSplit) regs_inc<C::kRegsScale>();
     const int w = warp - C::kWide, quad = w & 3;
     const int row = quad * 32 + lane;
     const int col0 = (w >> 2) * C::kCols;
@@ -332,37 +407,52 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
       const int n = (tile % P.tiles_n) * kW4M + row;
       const int tb = (tile / P.tiles_n) * NT;
       const int g0 = kb0 * C::kGroups, g1 = kb1 * C::kGroups;
-      // a group's scale, four groups ahead, as loaded
-      auto scale_of = [&](int g) -> uint16_t {
-        return n < p.N && g < g1 && (g << GS) < p.K ? __ldg(p.s + g * p.ld_s + n) : uint16_t(0);
+      // The scales of the next four groups, loaded while these four are added
+      // (behind the last group, that one's: a selection would wait for the load).
+      const int last_g = (p.K - 1) >> GS;
+      const uint16_t* s_row = p.s + min(n, p.N - 1);
+      uint32_t sq[4], sn[4];
+      auto scales = [&](int g) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sn[u] = ld_early(s_row + min(g + u, last_g) * p.ld_s);
       };
-      float acc[C::kCols];
+      scales(g0);
+      uint64_t acc[C::kCols / 2];  // pairs of sums
 #pragma unroll
-      for (int c = 0; c < C::kCols; ++c) acc[c] = 0.f;
-      uint16_t sq[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) sq[u] = scale_of(g0 + u);
+      for (int c = 0; c < C::kCols / 2; ++c) acc[c] = 0;
       for (int g = g0; g < g1 && ok; g += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sq[u] = sn[u];
+        scales(g + 4);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if (g + u >= g1 || !ok) break;
-          ok = mbar_wait(dfull0 + 8 * db.i, db.fill());
+          ok = role_wait(dfull0 + 8 * db.i, db.fill());
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const float sc = X8 ? E::bits_to_f32(sq[u]) * 64.f : E::bits_to_f32(sq[u]);
-          sq[u] = scale_of(g + u + 4);
+          // a group behind K has sums of 0, whatever the last scale is
+          const float s1 = g + u <= last_g ? E::bits_to_f32(static_cast<uint16_t>(sq[u])) : 0.f;
+          const float sc = X8 ? s1 * 64.f : s1;
           tc_fence_after();
+          // some columns at a time, and the accumulator is free before the
+          // last ones' arithmetic
+          constexpr int kLoad = C::kCols == 32 ? 32 : 16;
+          const uint64_t sc2 = pack2(sc, sc);
 #pragma unroll
-          for (int c = 0; c < C::kCols; c += 16) {
-            float v[16];
-            tmem_ld16(dsrc + db.i * NT + c, v);
+          for (int c0 = 0; c0 < C::kCols; c0 += kLoad) {
+            float v[kLoad / 16][16];
+#pragma unroll
+            for (int c = 0; c < kLoad; c += 16) tmem_ld16(dsrc + db.i * NT + c0 + c, v[c / 16]);
             tmem_ld_wait();
+            if (c0 + kLoad == C::kCols) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(dempty0 + 8 * db.i);
+            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(sc, v[i], acc[c + i]);
+            for (int c = 0; c < kLoad; c += 2)
+              fma2(acc[(c0 + c) / 2], pack2(v[c / 16][c % 16], v[c / 16][c % 16 + 1]), sc2);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(dempty0 + 8 * db.i);
           db.next(C::kDBufs);
         }
       }
@@ -373,7 +463,9 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
           for (int c = 0; c < C::kCols; ++c) {
             const int t = tb + col0 + c;
             if (t < p.tok) {
-              const float v = X8 ? acc[c] * __ldg(p.x_scale + t) : acc[c];
+              const float2 f = unpack2(acc[c / 2]);
+              const float a = c & 1 ? f.y : f.x;
+              const float v = X8 ? a * __ldg(p.x_scale + t) : a;
               stg16(p.out + t * p.ld_out + n, E::f32_to_bits(v));
             }
           }
@@ -383,17 +475,22 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
         // are all done
         float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int c = 0; c < C::kCols; ++c) part[(col0 + c) * kW4M + row] = acc[c];
+        for (int c = 0; c < C::kCols; c += 2) {
+          const float2 f = unpack2(acc[c / 2]);
+          part[(col0 + c) * kW4M + row] = f.x;
+          part[(col0 + c + 1) * kW4M + row] = f.y;
+        }
       }
     }
   } else if (warp == C::kTmaWarp) {
     // =========================== TMA
+    if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
     RingPos st;
     int issued = 0;
     for (int tile = first; tile < tiles && ok; tile += step) {
       const int n0 = (tile % P.tiles_n) * kW4M, tb = (tile / P.tiles_n) * NT;
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = mbar_wait(empty0 + 8 * st.i, st.drain());
+        ok = role_wait(empty0 + 8 * st.i, st.drain());
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t dst = sbase + st.i * C::kStage, bar = full0 + 8 * st.i;
@@ -411,8 +508,11 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     // after a wait that gave up: the copies still in flight
     if (!ok)
       for (int i = max(0, issued - P.stages); i < issued; ++i)
-        mbar_wait(full0 + 8 * (i % P.stages), (i / P.stages) & 1);
+        role_wait(full0 + 8 * (i % P.stages), (i / P.stages) & 1);
+  } else if (warp > C::kMmaWarp + 1) {
+    if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
   } else {
+    if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
     // =========================== MMA: group i of the CTA is warp i % 2's
     const int mw = warp - C::kMmaWarp;
     constexpr int kSteps = X8 ? 4 : 8;           // MMAs of a block
@@ -424,14 +524,14 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     for (int tile = first; tile < tiles && ok; tile += step) {
       for (int kb = kb0; kb < kb1 && ok; ++kb, ++blk) {
         if (C::kGroups > 1 || (blk & 1) == static_cast<uint32_t>(mw)) {
-          ok = mbar_wait(full0 + 8 * st.i, st.fill()) && mbar_wait(afull0 + 8 * ab.i, ab.fill());
+          ok = role_wait(full0 + 8 * st.i, st.fill()) && role_wait(afull0 + 8 * ab.i, ab.fill());
           // addresses in a descriptor are in units of 16 bytes
           const uint64_t bd = bd0 + static_cast<uint32_t>(st.i * (C::kStage / 16));
           const uint32_t at = abase + ab.i * C::kACols;
 #pragma unroll
           for (int j = 0; j < C::kGroups; ++j) {
             if (C::kGroups == 1 || (j & 1) == mw) {
-              ok = ok && mbar_wait(dempty0 + 8 * db.i, db.drain());
+              ok = ok && role_wait(dempty0 + 8 * db.i, db.drain());
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
