@@ -338,7 +338,6 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
   P.nkb = (a.K + lora::kW4K - 1) / lora::kW4K;
   const int64_t tiles = static_cast<int64_t>(P.tiles_n) * P.tiles_t;
   if (tiles > (1 << 28)) return LORA_ERR_UNSUPPORTED;
-  P.cs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(8, P.nkb), sms / tiles)));
   // all 512 TMEM columns: with this much shared memory no other block that
   // takes TMEM fits beside it (they ask for kTmemCtaMinSmem at least)
   const int fixed = 1024 + 256 + 8 * 64;
@@ -359,18 +358,35 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
   if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem,
                      C::kSplit ? C::kRegs : 0))
     return LORA_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(P.cs > 1 ? tiles * P.cs : std::min<int64_t>(tiles, sms)));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  LaunchAttrs la;
-  if (P.cs > 1) la.cluster(static_cast<unsigned>(P.cs));
-  la.apply(cfg);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
-  ++g_launches;
+  // Whole rounds of one tile for each SM; the tiles left over share the SMs by
+  // splitting their K range over clusters, in a launch of their own that takes
+  // SMs as the first one's blocks leave them.
+  auto launch = [&](int64_t lo, int64_t hi, bool after) {
+    P.tile0 = static_cast<int>(lo);
+    P.tile1 = static_cast<int>(hi);
+    P.cs = static_cast<int>(
+        std::max<int64_t>(1, std::min<int64_t>(std::min(8, P.nkb), sms / (hi - lo))));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(
+        static_cast<unsigned>(P.cs > 1 ? (hi - lo) * P.cs : std::min<int64_t>(hi - lo, sms)));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    LaunchAttrs la;
+    if (P.cs > 1) la.cluster(static_cast<unsigned>(P.cs));
+    if (after) la.programmatic();
+    la.apply(cfg);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+    ++g_launches;
+    return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  };
+  const int64_t left = tiles % sms;
+  const bool split = tiles > sms && left > 0 && left <= sms / 2 && P.nkb > 1;
+  const int64_t whole = split ? tiles - left : tiles;
+  lora_status s = launch(0, whole, false);
+  if (s == LORA_OK && split) s = launch(whole, tiles, true);
   g_last_path = LORA_PATH_TENSOR | (P.cs > 1 ? LORA_PATH_SPLITK : 0);
-  return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  return s;
 }
 
 template <class E, bool X8, int GS>

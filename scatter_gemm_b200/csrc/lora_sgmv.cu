@@ -265,6 +265,9 @@ struct LaunchAttrs {
   }
   void after_grouping(const Grouping& g) {
     if (!LORA_PDL || g.vseg_indptr == nullptr) return;
+    programmatic();
+  }
+  void programmatic() {
     a[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a[n].val.programmaticStreamSerializationAllowed = 1;
     ++n;

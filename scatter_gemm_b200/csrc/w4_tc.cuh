@@ -44,6 +44,7 @@ struct W4TcParams {
   int tiles_n, tiles_t;  // tiles of weight rows and of tokens
   int nkb;               // K blocks
   int cs;                // CTAs of a cluster, which share a tile's K blocks
+  int tile0, tile1;      // this launch's tiles
   int stages;
   uint32_t idesc;
 };
@@ -255,6 +256,8 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   uint32_t* tmem_slot =
       reinterpret_cast<uint32_t*>(bars + 2 * P.stages + 2 * C::kABufs + 2 * C::kDBufs);
 
+  // the launch of the last tiles may take SMs as this one's blocks leave them
+  griddep_launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < P.stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -292,8 +295,8 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   const uint32_t abase = tmem + C::kDBufs * NT;
   const int rank = P.cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int kb0 = P.nkb * rank / P.cs, kb1 = P.nkb * (rank + 1) / P.cs;
-  const int tiles = P.tiles_n * P.tiles_t;
-  const int first = blockIdx.x / P.cs, step = gridDim.x / P.cs;
+  const int tiles = P.tile1;
+  const int first = P.tile0 + blockIdx.x / P.cs, step = gridDim.x / P.cs;
   bool ok = true;
 
   if (warp < C::kWide) {
@@ -482,6 +485,35 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
         }
       }
     }
+    if (P.cs > 1) {
+      // One tile: the parts of the cluster's CTAs, each CTA adding its share of
+      // the tokens in rank order.  A CTA whose waits gave up has recorded it.
+      cluster_sync();
+      const int tb = (first / P.tiles_n) * NT, n0 = (first % P.tiles_n) * kW4M;
+      const int c0 = NT * rank / P.cs, c1 = NT * (rank + 1) / P.cs;
+      for (int e = 32 * w + lane; e < (c1 - c0) * (kW4M / 4); e += 32 * SW) {
+        // four rows of a token; all ranks' loads before the first sum
+        const int c = c0 + e / (kW4M / 4), r = e % (kW4M / 4) * 4;
+        const int t = tb + c;
+        if (t >= p.tok || !ok) continue;
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < P.cs)
+            v[i] = ld_dsmem_v4(mapa_shared(sbase + static_cast<uint32_t>(c * kW4M + r) * 4, i));
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+          if (i < P.cs) {
+            v[0].x += v[i].x; v[0].y += v[i].y; v[0].z += v[i].z; v[0].w += v[i].w;
+          }
+        const float f = X8 ? __ldg(p.x_scale + t) : 1.f;
+        const float o[4] = {v[0].x * f, v[0].y * f, v[0].z * f, v[0].w * f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n0 + r + i < p.N) stg16(p.out + t * p.ld_out + n0 + r + i, E::f32_to_bits(o[i]));
+      }
+      cluster_sync_relaxed();
+    }
   } else if (warp == C::kTmaWarp) {
     // =========================== TMA
     if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
@@ -562,24 +594,9 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   }
   __syncwarp();
 
-  if (P.cs > 1) {
-    // one tile: the parts of the cluster's CTAs, each CTA adding its share of
-    // the tokens in rank order
-    ok = __syncthreads_and(ok);
+  if (P.cs > 1 && (warp < C::kWide || warp >= C::kTmaWarp)) {
+    // the scaling warps' barriers before and after they read the parts
     cluster_sync();
-    const int tb = (first / P.tiles_n) * NT, n0 = (first % P.tiles_n) * kW4M;
-    const int c0 = NT * rank / P.cs, c1 = NT * (rank + 1) / P.cs;
-    for (int e = tid; e < (c1 - c0) * kW4M; e += C::kThreads) {
-      const int c = c0 + e / kW4M, r = e % kW4M;
-      const int t = tb + c, n = n0 + r;
-      if (t < p.tok && n < p.N && ok) {
-        float v = 0.f;
-        for (int i = 0; i < P.cs; ++i)
-          v += ld_dsmem_f32(mapa_shared(sbase + static_cast<uint32_t>(c * kW4M + r) * 4, i));
-        if (X8) v *= __ldg(p.x_scale + t);
-        stg16(p.out + t * p.ld_out + n, E::f32_to_bits(v));
-      }
-    }
     cluster_sync_relaxed();
   }
   __syncthreads();
@@ -587,6 +604,8 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
+  // a launch that began early ends after the one before it
+  griddep_wait();
 }
 
 }  // namespace lora
