@@ -13,7 +13,7 @@
 #include <type_traits>
 
 #ifndef LORA_W4_MV_TOKENS
-#define LORA_W4_MV_TOKENS 16 // 4-bit projection: tokens up to which w4_mv runs
+#define LORA_W4_MV_TOKENS 8  // 4-bit projection: tokens up to which w4_mv runs
 #endif
 
 namespace {
@@ -303,18 +303,17 @@ lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
   const int64_t blocks = (a.K + 127) / 128;
   const int tiles = (a.N + 15) / 16;
   const int per_sm = WARPS == 8 ? LORA_MV_OCC : 1;
-  // staged x and sums of x for tt tokens, parts of the tiles for n blocks an SM
+  // staged x and sums of x for tt tokens, and two tiles' parts
   int tt = std::min(a.tok, 8 * NT);
-  auto run = [&](int n) { return std::min((tiles + sms * n - 1) / (sms * n), lora::kMvTiles); };
-  auto bytes = [&](int n) {
+  auto bytes = [&]() {
     return tt * static_cast<int64_t>(lora::mv_row_bytes(static_cast<int>(blocks) * 128)) +
-           blocks * (4 / VW) * NT * 32 + (run(n) + WARPS - 1) * NT * 512;
+           blocks * (4 / VW) * NT * 32 + 2 * WARPS * NT * 512;
   };
-  while (tt > 1 && bytes(1) > kMvSmem) --tt;
-  if (bytes(1) > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
+  while (tt > 1 && bytes() > kMvSmem) --tt;
+  if (bytes() > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
   int occ = per_sm;
-  while (occ > 1 && occ * (bytes(occ) + 1024) > 227 * 1024) --occ;
-  const int smem = static_cast<int>(bytes(occ));
+  const int smem = static_cast<int>(bytes());
+  while (occ > 1 && occ * (smem + 1024) > 227 * 1024) --occ;
   const int64_t gy = (a.tok + tt - 1) / tt;
   if (gy > 65535) return LORA_ERR_UNSUPPORTED;
   const dim3 grid(std::min(tiles, sms * occ), static_cast<unsigned>(gy));
@@ -325,6 +324,39 @@ lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
   ++g_launches;
   g_last_path = LORA_PATH_GENERAL;
   return launch_status();
+}
+
+// Clusters of 1 .. 8 blocks of one SM each that the current device holds at
+// once (fewer than its SMs over the size, where that does not divide a GPC's).
+struct ClusterFacts {
+  std::atomic<int> ready{0};
+  int most[9] = {0};
+};
+ClusterFacts g_clusters[kMaxDevices];
+
+template <class K>
+const int* cluster_counts(K kernel, int threads, size_t smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  ClusterFacts& f = g_clusters[dev];
+  if (f.ready.load(std::memory_order_acquire)) return f.most;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  if (!f.ready.load(std::memory_order_relaxed)) {
+    for (int cs = 1; cs <= 8; ++cs) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(64 * cs);
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      LaunchAttrs la;
+      la.cluster(cs);
+      la.apply(cfg);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) f.most[cs] = n;
+      cudaGetLastError();  // a failed query must not leave a sticky launch error
+    }
+    f.ready.store(1, std::memory_order_release);
+  }
+  return f.most;
 }
 
 template <class E, bool X8, int NT, int GS, int SETS, int SW>
@@ -358,14 +390,29 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
   if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem,
                      C::kSplit ? C::kRegs : 0))
     return LORA_ERR_CUDA;
+  const int* most = cluster_counts(kernel, C::kThreads, smem);
+  if (!most) return LORA_ERR_CUDA;
   // Whole rounds of one tile for each SM; the tiles left over share the SMs by
   // splitting their K range over clusters, in a launch of their own that takes
   // SMs as the first one's blocks leave them.
   auto launch = [&](int64_t lo, int64_t hi, bool after) {
     P.tile0 = static_cast<int>(lo);
     P.tile1 = static_cast<int>(hi);
-    P.cs = static_cast<int>(
-        std::max<int64_t>(1, std::min<int64_t>(std::min(8, P.nkb), sms / (hi - lo))));
+    // Least rounds x (blocks of K each + 4): a round's set-up and the adding up
+    // of the parts cost about as much as four blocks.
+    P.cs = 1;
+    if (hi - lo < sms) {
+      int64_t best = P.nkb + 4;
+      for (int cs = 2; cs <= std::min(8, P.nkb); ++cs) {
+        if (most[cs] < 1) continue;
+        const int64_t cost =
+            (hi - lo + most[cs] - 1) / most[cs] * ((P.nkb + cs - 1) / cs + 4);
+        if (cost < best) {
+          best = cost;
+          P.cs = cs;
+        }
+      }
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(
         static_cast<unsigned>(P.cs > 1 ? (hi - lo) * P.cs : std::min<int64_t>(hi - lo, sms)));
@@ -381,7 +428,9 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
     return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
   };
   const int64_t left = tiles % sms;
-  const bool split = tiles > sms && left > 0 && left <= sms / 2 && P.nkb > 1;
+  // (Up to 64 tokens a second round of whole tiles, which has the memory to
+  // itself, is the shorter: 31.7 against 33.7 us at 32 tokens x 4096 x 24576.)
+  const bool split = NT > 64 && tiles > sms && left > 0 && left <= sms / 2 && P.nkb > 1;
   const int64_t whole = split ? tiles - left : tiles;
   lora_status s = launch(0, whole, false);
   if (s == LORA_OK && split) s = launch(whole, tiles, true);

@@ -136,7 +136,6 @@ template <> struct MvScale<Fp16> {
 #define LORA_MV_DEPTH 4
 #endif
 constexpr int kMvDepth = LORA_MV_DEPTH;  // blocks of 128 K that a warp has in flight
-constexpr int kMvTiles = 16;             // row tiles of a block between two passes over their parts
 
 // Bytes between the staged rows of x: a multiple of 128 plus 64, so that the
 // two tokens that a quarter of a warp reads lie in different banks.
@@ -166,10 +165,10 @@ struct MvBlock {
 // 4*VW bytes and the 16 values of a product lie in one group of 32*VW weights:
 // VW = 4, 2, 1 for groups of 128, 64, 32.
 //
-// A block owns a run of row tiles, and its warps share the run's blocks of
-// 16 x 128 weights evenly, in order, across tile borders: a warp's parts of its
-// tiles go to shared memory, and one pass at the end adds each tile's parts in
-// that order.
+// A block owns a run of row tiles, and its warps take the run's blocks of
+// 16 x 128 weights in turn, on across tile borders, so that together they read
+// neighbouring pieces of the same rows.  At the end of a tile the warps' parts
+// meet in shared memory and are added in the warps' order.
 //
 // grid = (runs of row tiles, token tiles of `tt` tokens).
 template <class E, bool X8, int NT, int VW, int WARPS>
@@ -187,7 +186,7 @@ w4_mv_kernel(const W4Args p, const int tt) {
   const int blocks = (p.K + 127) / 128;
   const int rowb = mv_row_bytes(blocks * 128);
   float* xs = reinterpret_cast<float*>(mv_smem + tt * rowb);  // [groups][8 NT]: sums of x / kOut
-  float* part = xs + blocks * kSub * 8 * NT;                  // [tiles + WARPS - 1][8 NT][16]
+  float* part = xs + blocks * kSub * 8 * NT;                  // [2][WARPS][8 NT][16]
   const int tiles = (p.N + 15) / 16;
   const int run0 = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.x / gridDim.x);
   const int run1 = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -195,126 +194,107 @@ w4_mv_kernel(const W4Args p, const int tt) {
   const int last_g = (p.K - 1) >> p.group_shift;
   const uint32_t ld_s = static_cast<uint32_t>(p.ld_s);
 
-  for (int r0 = run0; r0 < run1; r0 += kMvTiles) {
-    const int ntiles = min(kMvTiles, run1 - r0);
-    const int total = ntiles * blocks;
-    const int act = min(WARPS, total);  // warps with blocks
-    const int first = min(total * warp / act, total - 1);
-    const int left0 = warp < act ? total * (warp + 1) / act - first : 0;
-
-    // The next block to fetch: its tile, its place in K and the lane's two
-    // rows.  Columns behind a row's end are read at its last words: x is 0
-    // there, and any weight will do.
-    MvBlock buf[kMvDepth];
+  // The next block to fetch: its tile, its place in K and the lane's two rows.
+  // Columns behind a row's end are read at its last words: x is 0 there, and
+  // any weight will do.
+  MvBlock buf[kMvDepth];
 #pragma unroll
-    for (int d = 0; d < kMvDepth; ++d) buf[d].z[0] = buf[d].z[1] = 8;
-    int f_left = left0, f_tile = first / blocks, f_blk = first - f_tile * blocks;
-    const uint8_t* f_w[2];
-    const uint16_t* f_s[2];
-    int f_row[2];
-    auto rows_of = [&](int tile) {
+  for (int d = 0; d < kMvDepth; ++d) buf[d].z[0] = buf[d].z[1] = 8;
+  int f_tile = run0, f_blk = warp;
+  const uint8_t* f_w[2];
+  const uint16_t* f_s[2];
+  int f_row[2];
+  auto rows_of = [&](int tile) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f_row[h] = min((r0 + tile) * 16 + g + 8 * h, p.N - 1);
-        f_w[h] = p.w + f_row[h] * p.ld_w;
-        f_s[h] = p.s + f_row[h];
-      }
-    };
-    rows_of(f_tile);
-    auto fetch = [&](MvBlock& b) {
-      if (f_left > 0) {
-        --f_left;
+    for (int h = 0; h < 2; ++h) {
+      f_row[h] = min(tile * 16 + g + 8 * h, p.N - 1);
+      f_w[h] = p.w + f_row[h] * p.ld_w;
+      f_s[h] = p.s + f_row[h];
+    }
+  };
+  auto skip = [&]() {  // on to the tile that holds block f_blk
+    if (f_blk >= blocks) {
+      do {
+        f_blk -= blocks;
+        ++f_tile;
+      } while (f_blk >= blocks);
+      rows_of(f_tile);
+    }
+  };
+  rows_of(f_tile);
+  skip();
+  auto fetch = [&](MvBlock& b) {
+    if (f_tile < run1) {
 #pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          const uint32_t col = min(f_blk * 64 + (sub * 16 + t4 * 4) * VW, last_col);
+      for (int sub = 0; sub < kSub; ++sub) {
+        const uint32_t col = min(f_blk * 64 + (sub * 16 + t4 * 4) * VW, last_col);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t* src = f_w[h] + col;
-            if constexpr (VW == 4) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-              b.w[h][0] = v.x; b.w[h][1] = v.y; b.w[h][2] = v.z; b.w[h][3] = v.w;
-            } else if constexpr (VW == 2) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-              b.w[h][2 * sub] = v.x; b.w[h][2 * sub + 1] = v.y;
-            } else {
-              b.w[h][sub] = __ldg(reinterpret_cast<const uint32_t*>(src));
-            }
-          }
-        }
-        const uint32_t gi = min(f_blk * kSub + (t4 & (kSub - 1)), last_g);
-        const uint64_t si = static_cast<uint64_t>(gi) * ld_s;
-        b.s[0] = __ldg(f_s[0] + si);
-        b.s[1] = __ldg(f_s[1] + si);
-        if (p.z) {
-          const uint8_t* z = p.z + si;
-          b.z[0] = __ldg(z + f_row[0]);
-          b.z[1] = __ldg(z + f_row[1]);
-        }
-        if (++f_blk == blocks) {
-          f_blk = 0;
-          rows_of(++f_tile);
-        }
-      }
-    };
-#pragma unroll
-    for (int d = 0; d < kMvDepth; ++d) fetch(buf[d]);
-
-    if (r0 == run0) {
-      // x: chunks of eight values, zeros behind K; within a block of 32*VW
-      // values chunk c lies at (c % VW) * 4 + c / VW, so that the four lanes
-      // of a token read 64 neighbouring bytes
-      const int cpr = blocks * 16;
-      const int units = ntok * cpr;
-      int r = tid / cpr, c = tid - r * cpr;
-      for (int u0 = 0; u0 < units; u0 += kThreads) {
-        const bool live = u0 + tid < units;
-        const int k = c * 8;
-        const int left = live ? min(8, p.K - k) : 0;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        uint32_t* o = reinterpret_cast<uint32_t*>(&v);
-        if (left > 0) {
-          const int64_t at = (t0 + r) * p.ld_x + k;
-          if (X8) {
-            const uint8_t* src = static_cast<const uint8_t*>(p.x) + at;
-            uint32_t b[2] = {0, 0};
-            if (left == 8 && (reinterpret_cast<uintptr_t>(src) & 7) == 0) {
-              const uint2 d = __ldg(reinterpret_cast<const uint2*>(src));
-              b[0] = d.x; b[1] = d.y;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (i < left) b[i / 4] |= static_cast<uint32_t>(__ldg(src + i)) << (8 * (i & 3));
-            }
-            const uint2 lo = w4_from_e4m3<C>(b[0]), hi = w4_from_e4m3<C>(b[1]);
-            v = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* src = f_w[h] + col;
+          if constexpr (VW == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+            b.w[h][0] = v.x; b.w[h][1] = v.y; b.w[h][2] = v.z; b.w[h][3] = v.w;
+          } else if constexpr (VW == 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+            b.w[h][2 * sub] = v.x; b.w[h][2 * sub + 1] = v.y;
           } else {
-            const uint16_t* src = static_cast<const uint16_t*>(p.x) + at;
-            if (left == 8 && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-              v = __ldg(reinterpret_cast<const uint4*>(src));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (i < left) o[i / 2] |= static_cast<uint32_t>(__ldg(src + i)) << (16 * (i & 1));
-            }
+            b.w[h][sub] = __ldg(reinterpret_cast<const uint32_t*>(src));
           }
         }
-        float sum = 0.f;
+      }
+      const uint32_t gi = min(f_blk * kSub + (t4 & (kSub - 1)), last_g);
+      const uint64_t si = static_cast<uint64_t>(gi) * ld_s;
+      b.s[0] = __ldg(f_s[0] + si);
+      b.s[1] = __ldg(f_s[1] + si);
+      if (p.z) {
+        const uint8_t* z = p.z + si;
+        b.z[0] = __ldg(z + f_row[0]);
+        b.z[1] = __ldg(z + f_row[1]);
+      }
+      f_blk += WARPS;
+      skip();
+    }
+  };
+
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = C::u32_to_f2(o[i]);
-          sum += f.x + f.y;
-          if (MvScale<C>::kX != 1.f)
-            o[i] = C::f2_to_u32(f.x * MvScale<C>::kX, f.y * MvScale<C>::kX);
-        }
-        // the 4*VW lanes of a group add their chunks
+  for (int d = 0; d < kMvDepth; ++d) fetch(buf[d]);
+
+  {
+    // x: chunks of eight values, zeros behind K; within a block of 32*VW
+    // values chunk c lies at (c % VW) * 4 + c / VW, so that the four lanes
+    // of a token read 64 neighbouring bytes
+    const int cpr = blocks * 16;
+    const int units = ntok * cpr;
+    const uint8_t* xb = static_cast<const uint8_t*>(p.x);
+    constexpr int kEl = X8 ? 1 : 2, kPiece = 8 * kEl;  // bytes of a value, of a chunk
+    // kBatch chunks a thread at a time, all of their loads first: whole chunks
+    // as the one or two aligned pieces that cover them
+    constexpr int kBatch = 4;
+    int r = tid / cpr, c = tid - r * cpr;
+    for (int u0 = 0; u0 < units; u0 += kBatch * kThreads) {
+      uint4 lo[kBatch], hi[kBatch];
+      int rr[kBatch], cc[kBatch];
 #pragma unroll
-        for (int d = 2 * VW; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (live) {
-          const int in = c & (4 * VW - 1);
-          if (in == 0) xs[c / (4 * VW) * (8 * NT) + r] = sum * (1.f / MvScale<C>::kOut);
-          const int at = (c - in) + (in % VW) * 4 + in / VW;
-          // a product takes pairs 0 and 2 or 1 and 3 of a word: neighbours here
-          *reinterpret_cast<uint4*>(mv_smem + r * rowb + at * 16) = make_uint4(v.x, v.z, v.y, v.w);
+      for (int i = 0; i < kBatch; ++i) {
+        rr[i] = r;
+        cc[i] = c;
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        if (u0 + i * kThreads + tid < units && p.K - c * 8 >= 8) {
+          const uint8_t* src = xb + ((t0 + r) * p.ld_x + c * 8) * kEl;
+          const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & (kPiece - 1));
+          if constexpr (X8) {
+            const uint2* q = reinterpret_cast<const uint2*>(src - off);
+            const uint2 d = __ldg(q);
+            lo[i].x = d.x; lo[i].y = d.y;
+            if (off) {
+              const uint2 e = __ldg(q + 1);
+              hi[i].x = e.x; hi[i].y = e.y;
+            }
+          } else {
+            const uint4* q = reinterpret_cast<const uint4*>(src - off);
+            lo[i] = __ldg(q);
+            if (off) hi[i] = __ldg(q + 1);
+          }
         }
         c += kThreads;
         while (c >= cpr) {
@@ -322,96 +302,153 @@ w4_mv_kernel(const W4Args p, const int tt) {
           ++r;
         }
       }
-    }
-    __syncthreads();
-
-    // columns of the product behind the last token repeat one and are not read
-    const uint8_t* xr[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xr[n] = mv_smem + min(8 * n + g, ntok - 1) * rowb + t4 * 16;
-
-    float acc[NT][4];
+      for (int i = 0; i < kBatch; ++i) {
+        const bool live = u0 + i * kThreads + tid < units;
+        const int left = live ? p.K - cc[i] * 8 : 0;
+        const uint8_t* src = xb + ((t0 + rr[i]) * p.ld_x + cc[i] * 8) * kEl;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & (kPiece - 1));
+        uint4 v = lo[i];
+        uint32_t* o = reinterpret_cast<uint32_t*>(&v);
+        if constexpr (X8) {
+          uint64_t b = (static_cast<uint64_t>(lo[i].y) << 32 | lo[i].x) >> (8 * off);
+          if (off) b |= (static_cast<uint64_t>(hi[i].y) << 32 | hi[i].x) << (64 - 8 * off);
+          if (left > 0 && left < 8)
+            for (int e = 0; e < left; ++e) b |= static_cast<uint64_t>(__ldg(src + e)) << (8 * e);
+          const uint2 x = w4_from_e4m3<C>(static_cast<uint32_t>(b));
+          const uint2 y = w4_from_e4m3<C>(static_cast<uint32_t>(b >> 32));
+          v = make_uint4(x.x, x.y, y.x, y.y);
+        } else {
+          if (off) v = bytes_at(lo[i], hi[i], off);
+          if (left > 0 && left < 8) {
+            v = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    int left = left0, slot = first / blocks + warp, blk = first % blocks;
-    while (left > 0) {
-#pragma unroll
-      for (int d = 0; d < kMvDepth; ++d) {
-        if (left <= 0) break;
-        const MvBlock& b = buf[d];
-        const uint32_t sz[2] = {b.s[0] | (b.z[0] << 16), b.s[1] | (b.z[1] << 16)};
-#pragma unroll
-        for (int sub = 0; sub < kSub; ++sub) {
-          uint32_t sz0 = sz[0], sz1 = sz[1];
-          if (kSub > 1) {
-            sz0 = __shfl_sync(0xffffffffu, sz0, (lane & ~3) + sub);
-            sz1 = __shfl_sync(0xffffffffu, sz1, (lane & ~3) + sub);
-          }
-          float g1[NT][4], g2[NT][4];
-#pragma unroll
-          for (int j = 0; j < VW; ++j) {
-            constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;  // q, 16 q
-            const uint32_t a = b.w[0][sub * VW + j], e = b.w[1][sub * VW + j];
-            const uint32_t a8 = a >> 8, e8 = e >> 8;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 xv =
-                  *reinterpret_cast<const uint4*>(xr[n] + blk * 256 + (sub * VW + j) * 64);
-              w4_mma<C>(g1[n], a & kLo, e & kLo, a8 & kLo, e8 & kLo, xv.x, xv.y, j == 0);
-              w4_mma<C>(g2[n], a & kHi, e & kHi, a8 & kHi, e8 & kHi, xv.z, xv.w, j == 0);
-            }
-          }
-          const float s0 = E::bits_to_f32(static_cast<uint16_t>(sz0));
-          const float s1 = E::bits_to_f32(static_cast<uint16_t>(sz1));
-          const float z0 = -static_cast<float>((sz0 >> 16) & 15);
-          const float z1 = -static_cast<float>((sz1 >> 16) & 15);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float2 x2 = *reinterpret_cast<const float2*>(xs + (blk * kSub + sub) * (8 * NT) +
-                                                               8 * n + 2 * t4);
-            acc[n][0] = fmaf(s0, fmaf(z0, x2.x, fmaf(g2[n][0], 0.0625f, g1[n][0])), acc[n][0]);
-            acc[n][1] = fmaf(s0, fmaf(z0, x2.y, fmaf(g2[n][1], 0.0625f, g1[n][1])), acc[n][1]);
-            acc[n][2] = fmaf(s1, fmaf(z1, x2.x, fmaf(g2[n][2], 0.0625f, g1[n][2])), acc[n][2]);
-            acc[n][3] = fmaf(s1, fmaf(z1, x2.y, fmaf(g2[n][3], 0.0625f, g1[n][3])), acc[n][3]);
+            for (int e = 0; e < 8; ++e)
+              if (e < left)
+                o[e / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + e))
+                            << (16 * (e & 1));
           }
         }
-        fetch(buf[d]);
-        --left;
-        if (++blk == blocks || left == 0) {
-          // this warp's part of a tile: slot = tile + warp, in the blocks' order
-          blk = 0;
-          float* o = part + slot++ * kPart + 2 * t4 * 16 + g;
+        float sum = 0.f;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            o[n * 128] = acc[n][0];
-            o[n * 128 + 16] = acc[n][1];
-            o[n * 128 + 8] = acc[n][2];
-            o[n * 128 + 24] = acc[n][3];
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = C::u32_to_f2(o[e]);
+          sum += f.x + f.y;
+          if (MvScale<C>::kX != 1.f)
+            o[e] = C::f2_to_u32(f.x * MvScale<C>::kX, f.y * MvScale<C>::kX);
+        }
+        // the 4*VW lanes of a group add their chunks
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-          }
+        for (int d = 2 * VW; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (live) {
+          const int in = cc[i] & (4 * VW - 1);
+          if (in == 0) xs[cc[i] / (4 * VW) * (8 * NT) + rr[i]] = sum * (1.f / MvScale<C>::kOut);
+          const int at = (cc[i] - in) + (in % VW) * 4 + in / VW;
+          // a product takes pairs 0 and 2 or 1 and 3 of a word: neighbours here
+          *reinterpret_cast<uint4*>(mv_smem + rr[i] * rowb + at * 16) =
+              make_uint4(v.x, v.z, v.y, v.w);
         }
       }
     }
+  }
+  __syncthreads();
+
+  // columns of the product behind the last token repeat one and are not read
+  const uint8_t* xr[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xr[n] = mv_smem + min(8 * n + g, ntok - 1) * rowb + t4 * 16;
+
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  int done = run0, par = 0;  // tiles before `done` are written
+  // every warp ends every tile, in order: the tile's parts, then its outputs
+  auto end_tile = [&]() {
+    float* rb = part + par * (WARPS * kPart);
+    par ^= 1;
+    float* o = rb + warp * kPart + 2 * t4 * 16 + g;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      o[n * 128] = acc[n][0];
+      o[n * 128 + 16] = acc[n][1];
+      o[n * 128 + 8] = acc[n][2];
+      o[n * 128 + 24] = acc[n][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    }
     __syncthreads();
-    for (int e = tid; e < ntiles * kPart; e += kThreads) {
-      const int tile = e / kPart, in = e % kPart;
-      const int tk = in >> 4, row = (r0 + tile) * 16 + (in & 15);
+    for (int e = tid; e < kPart; e += kThreads) {
+      const int tk = e >> 4, row = done * 16 + (e & 15);
       if (tk < ntok && row < p.N) {
-        // the warps that hold the tile's first and last block
-        const int w0 = (tile * blocks * act + act - 1) / total;
-        const int w1 = ((tile + 1) * blocks * act - 1) / total;
         float v = 0.f;
-        for (int w = w0; w <= w1; ++w) v += part[(tile + w) * kPart + in];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v += rb[w * kPart + e];
         v *= MvScale<C>::kOut;
         if (X8) v *= __ldg(p.x_scale + t0 + tk);
         stg16(p.out + (t0 + tk) * p.ld_out + row, E::f32_to_bits(v));
       }
     }
-    if (r0 + kMvTiles < run1) __syncthreads();
+    ++done;
+  };
+
+  int tile = run0, blk = warp;
+  while (blk >= blocks) {
+    blk -= blocks;
+    ++tile;
   }
+  while (tile < run1) {
+#pragma unroll
+    for (int d = 0; d < kMvDepth; ++d) {
+      if (tile >= run1) break;
+      while (done < tile) end_tile();
+      const MvBlock& b = buf[d];
+      const uint32_t sz[2] = {b.s[0] | (b.z[0] << 16), b.s[1] | (b.z[1] << 16)};
+#pragma unroll
+      for (int sub = 0; sub < kSub; ++sub) {
+        uint32_t sz0 = sz[0], sz1 = sz[1];
+        if (kSub > 1) {
+          sz0 = __shfl_sync(0xffffffffu, sz0, (lane & ~3) + sub);
+          sz1 = __shfl_sync(0xffffffffu, sz1, (lane & ~3) + sub);
+        }
+        float g1[NT][4], g2[NT][4];
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;  // q, 16 q
+          const uint32_t a = b.w[0][sub * VW + j], e = b.w[1][sub * VW + j];
+          const uint32_t a8 = a >> 8, e8 = e >> 8;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 xv =
+                *reinterpret_cast<const uint4*>(xr[n] + blk * 256 + (sub * VW + j) * 64);
+            w4_mma<C>(g1[n], a & kLo, e & kLo, a8 & kLo, e8 & kLo, xv.x, xv.y, j == 0);
+            w4_mma<C>(g2[n], a & kHi, e & kHi, a8 & kHi, e8 & kHi, xv.z, xv.w, j == 0);
+          }
+        }
+        const float s0 = E::bits_to_f32(static_cast<uint16_t>(sz0));
+        const float s1 = E::bits_to_f32(static_cast<uint16_t>(sz1));
+        const float z0 = -static_cast<float>((sz0 >> 16) & 15);
+        const float z1 = -static_cast<float>((sz1 >> 16) & 15);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 x2 = *reinterpret_cast<const float2*>(xs + (blk * kSub + sub) * (8 * NT) +
+                                                             8 * n + 2 * t4);
+          acc[n][0] = fmaf(s0, fmaf(z0, x2.x, fmaf(g2[n][0], 0.0625f, g1[n][0])), acc[n][0]);
+          acc[n][1] = fmaf(s0, fmaf(z0, x2.y, fmaf(g2[n][1], 0.0625f, g1[n][1])), acc[n][1]);
+          acc[n][2] = fmaf(s1, fmaf(z1, x2.x, fmaf(g2[n][2], 0.0625f, g1[n][2])), acc[n][2]);
+          acc[n][3] = fmaf(s1, fmaf(z1, x2.y, fmaf(g2[n][3], 0.0625f, g1[n][3])), acc[n][3]);
+        }
+      }
+      fetch(buf[d]);
+      blk += WARPS;
+      while (blk >= blocks) {
+        blk -= blocks;
+        ++tile;
+      }
+    }
+  }
+  while (done < run1) end_tile();
 }
 
 }  // namespace lora

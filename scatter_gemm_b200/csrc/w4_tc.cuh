@@ -258,19 +258,13 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
 
   // the launch of the last tiles may take SMs as this one's blocks leave them
   griddep_launch_dependents();
-  if (tid == 0) {
-    for (int s = 0; s < P.stages; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 4 + C::kMmaArrive);  // a set of widening warps and the MMAs
-    }
-    for (int s = 0; s < C::kABufs; ++s) {
-      mbar_init(afull0 + 8 * s, 4);
-      mbar_init(aempty0 + 8 * s, C::kMmaArrive);
-    }
-    for (int s = 0; s < C::kDBufs; ++s) {
-      mbar_init(dfull0 + 8 * s, 1);
-      mbar_init(dempty0 + 8 * s, SW);
-    }
+  // a barrier a thread, in the order of their addresses
+  if (tid < 2 * P.stages + 2 * C::kABufs + 2 * C::kDBufs) {
+    const int a = tid - 2 * P.stages, d = a - 2 * C::kABufs;
+    mbar_init(full0 + 8 * tid,
+              a < 0 ? (tid < P.stages ? 1 : 4 + C::kMmaArrive)   // a set of widening warps, the MMAs
+              : d < 0 ? (a < C::kABufs ? 4 : C::kMmaArrive)
+                      : (d < C::kDBufs ? 1 : SW));
     fence_mbar_init();
   }
   if (X8 && tid < 64) {
@@ -294,7 +288,8 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const uint32_t abase = tmem + C::kDBufs * NT;
   const int rank = P.cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int kb0 = P.nkb * rank / P.cs, kb1 = P.nkb * (rank + 1) / P.cs;
+  const int kb0 = P.cs > 1 ? P.nkb * rank / P.cs : 0;
+  const int kb1 = P.cs > 1 ? P.nkb * (rank + 1) / P.cs : P.nkb;
   const int tiles = P.tile1;
   const int first = P.tile0 + blockIdx.x / P.cs, step = gridDim.x / P.cs;
   bool ok = true;
