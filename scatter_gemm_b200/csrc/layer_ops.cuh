@@ -295,7 +295,7 @@ bool encode_w4(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kW4Smem = 225 * 1024;
+constexpr int kW4Smem = 227 * 1024;
 constexpr int kMvSmem = 200 * 1024;
 
 template <class E, bool X8, int NT, int VW, int WARPS>
@@ -372,9 +372,7 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
   if (tiles > (1 << 28)) return LORA_ERR_UNSUPPORTED;
   // all 512 TMEM columns: with this much shared memory no other block that
   // takes TMEM fits beside it (they ask for kTmemCtaMinSmem at least)
-  const int fixed = 1024 + 256 + 8 * 64;
-  P.stages = std::min(16, (220 * 1024 - fixed) / C::kStage) / C::kRing * C::kRing;
-  const size_t smem = std::max<size_t>(P.stages * C::kStage + fixed, 2 * kTmemCtaMinSmem);
+  constexpr size_t smem = std::max<size_t>(C::kSmem, 2 * kTmemCtaMinSmem);
   P.idesc = lora::make_idesc_f16(!X8 && std::is_same<E, lora::Bf16>::value ? 1 : 0, lora::kW4M, NT);
   const CUtensorMapDataType xt = X8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : std::is_same<E, lora::Bf16>::value

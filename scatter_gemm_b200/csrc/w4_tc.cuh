@@ -6,7 +6,7 @@
 // A tile is 128 weight rows x NT tokens; the weight rows are the rows of the
 // MMA, so that a weight's row is a lane of tensor memory (TMEM) and its scale a
 // scalar of the thread that owns the lane.  K goes in blocks of 128:
-//  - one warp loads the block's packed weights (8 KB) and x tile by TMA;
+//  - two warps load the blocks' packed weights (8 KB each) and x tiles by TMA;
 //  - sets of four widening warps, a block each in turn, turn the packed rows
 //    into q - z in the element type of x (exact: bf16, fp16, or e4m3 scaled by
 //    2^-6) and store them to TMEM, from where the MMA reads them: neither the
@@ -45,7 +45,6 @@ struct W4TcParams {
   int nkb;               // K blocks
   int cs;                // CTAs of a cluster, which share a tile's K blocks
   int tile0, tile1;      // this launch's tiles
-  int stages;
   uint32_t idesc;
 };
 
@@ -203,8 +202,7 @@ __device__ __forceinline__ bool elect_one() {
 template <bool X8, int NT, int GS, int SETS, int SW>
 struct W4Tc {
   static constexpr int kWide = 4 * SETS;                        // widening warps
-  static constexpr int kTmaWarp = kWide + SW, kMmaWarp = kTmaWarp + 1;
-  // the fourth of the last four warps only makes them a warpgroup
+  static constexpr int kTmaWarp = kWide + SW, kMmaWarp = kTmaWarp + 2;  // two of each
   static constexpr int kThreads = 32 * (kWide + SW + 4);
   static constexpr int kGroups = 128 >> GS;                     // groups of a block
   static constexpr int kACols = X8 ? 32 : 64;                   // TMEM columns of a widened block
@@ -219,7 +217,14 @@ struct W4Tc {
   static constexpr int kABufs = (kAFit < 8 ? kAFit : 8) / kRing * kRing;
   static constexpr int kWBytes = kW4M * 64;
   static constexpr int kXBytes = NT * (X8 ? 128 : 256);
-  static constexpr int kStage = kWBytes + kXBytes;
+  // Rings of packed weights and of x, apart: a widening set is done with the
+  // weights long before the MMA is with x.
+  static constexpr int kWStages = kXBytes > 16384 ? 4 : NT > 32 ? 8 : 12;
+  static constexpr int kXFit = (224 * 1024 - kWStages * kWBytes) / kXBytes / 2 * 2;
+  static constexpr int kXStages = kXFit < 12 ? kXFit : 12;
+  static constexpr int kAllBars = 2 * (kWStages + kXStages + kABufs + kDBufs);
+  static constexpr int kRings = kWStages * kWBytes + kXStages * kXBytes;
+  static constexpr int kSmem = 1024 + kRings + 256 + 8 * kAllBars + 16;
   static constexpr int kCols = NT / (SW / 4);                   // tokens of a scaling warp
   static constexpr int kMmaArrive = kGroups > 1 ? 2 : 1;        // MMA warps that share a block
   // With 64 sums a thread, the scaling warps take registers over from the
@@ -231,6 +236,7 @@ struct W4Tc {
   static_assert(!kSplit || kWide * kRegsWide + SW * kRegsScale + 4 * kRegsRest <=
                                (kWide + SW + 4) * kRegs,
                 "more registers than the block has");
+  static_assert(kWStages % kRing == 0 && kSmem <= 232448 && kRings >= NT * kW4M * 4, "rings");
   static_assert(kABufs >= kRing, "a widened block for each set");
 };
 
@@ -244,27 +250,32 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
-  // [ring of stages, later the split sums][code tables][barriers][TMEM address]
-  uint4* codes = reinterpret_cast<uint4*>(smem + P.stages * C::kStage);
+  // [weight stages][x stages], later the split sums, [code tables][barriers][TMEM address]
+  constexpr uint32_t kX0 = C::kWStages * C::kWBytes;
+  uint4* codes = reinterpret_cast<uint4*>(smem + C::kRings);
   uint64_t* bars = reinterpret_cast<uint64_t*>(codes + 16);
-  const uint32_t full0 = smem_u32(bars);
-  const uint32_t empty0 = full0 + 8 * P.stages;
-  const uint32_t afull0 = empty0 + 8 * P.stages;
+  const uint32_t wfull0 = smem_u32(bars);
+  const uint32_t wempty0 = wfull0 + 8 * C::kWStages;
+  const uint32_t xfull0 = wempty0 + 8 * C::kWStages;
+  const uint32_t xempty0 = xfull0 + 8 * C::kXStages;
+  const uint32_t afull0 = xempty0 + 8 * C::kXStages;
   const uint32_t aempty0 = afull0 + 8 * C::kABufs;
   const uint32_t dfull0 = aempty0 + 8 * C::kABufs;
   const uint32_t dempty0 = dfull0 + 8 * C::kDBufs;
-  uint32_t* tmem_slot =
-      reinterpret_cast<uint32_t*>(bars + 2 * P.stages + 2 * C::kABufs + 2 * C::kDBufs);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kAllBars);
 
   // the launch of the last tiles may take SMs as this one's blocks leave them
   griddep_launch_dependents();
   // a barrier a thread, in the order of their addresses
-  if (tid < 2 * P.stages + 2 * C::kABufs + 2 * C::kDBufs) {
-    const int a = tid - 2 * P.stages, d = a - 2 * C::kABufs;
-    mbar_init(full0 + 8 * tid,
-              a < 0 ? (tid < P.stages ? 1 : 4 + C::kMmaArrive)   // a set of widening warps, the MMAs
-              : d < 0 ? (a < C::kABufs ? 4 : C::kMmaArrive)
-                      : (d < C::kDBufs ? 1 : SW));
+  if (tid < C::kAllBars) {
+    int count = 1;  // a copy, or the MMAs of a group
+    const uint32_t at = wfull0 + 8 * tid;
+    if (at >= wempty0 && at < xfull0) count = 4;                    // a set of widening warps
+    if (at >= xempty0 && at < afull0) count = C::kMmaArrive;
+    if (at >= afull0 && at < aempty0) count = 4;
+    if (at >= aempty0 && at < dfull0) count = C::kMmaArrive;
+    if (at >= dempty0) count = SW;
+    mbar_init(at, count);
     fence_mbar_init();
   }
   if (X8 && tid < 64) {
@@ -304,7 +315,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
     // this set's blocks, every SETS-th of the CTA's, counted over its tiles
     RingPos st, ab;
     for (int i = 0; i < set; ++i) {
-      st.next(P.stages);
+      st.next(C::kWStages);
       ab.next(C::kABufs);
     }
     int skip = set;  // blocks of the next tile before this set's first
@@ -336,13 +347,15 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           if (kb >= kb1 || !ok) break;
-          ok = role_wait(full0 + 8 * st.i, st.fill());
+          ok = role_wait(wfull0 + 8 * st.i, st.fill());
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint8_t* src = smem + st.i * C::kStage + row * 64;
+          const uint8_t* src = smem + st.i * C::kWBytes + row * 64;
           uint4 pk[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) pk[c] = *reinterpret_cast<const uint4*>(src + ((c ^ rsw) << 4));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(wempty0 + 8 * st.i);
           ok = role_wait(aempty0 + 8 * ab.i, ab.drain());
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -381,11 +394,10 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(afull0 + 8 * ab.i);
-            mbar_arrive(empty0 + 8 * st.i);
           }
 #pragma unroll
           for (int i = 0; i < SETS; ++i) {
-            st.next(P.stages);
+            st.next(C::kWStages);
             ab.next(C::kABufs);
           }
           kb += SETS;
@@ -509,9 +521,12 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
       }
       cluster_sync_relaxed();
     }
-  } else if (warp == C::kTmaWarp) {
-    // =========================== TMA
+  } else if (warp < C::kMmaWarp) {
+    // =========================== TMA: a warp for the weights, one for x
     if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
+    const bool wt = warp == C::kTmaWarp;
+    const int stages = wt ? C::kWStages : C::kXStages;
+    const uint32_t full0 = wt ? wfull0 : xfull0, empty0 = wt ? wempty0 : xempty0;
     RingPos st;
     int issued = 0;
     for (int tile = first; tile < tiles && ok; tile += step) {
@@ -520,40 +535,43 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
         ok = role_wait(empty0 + 8 * st.i, st.drain());
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t dst = sbase + st.i * C::kStage, bar = full0 + 8 * st.i;
+        const uint32_t bar = full0 + 8 * st.i;
         if (elect_one()) {
-          mbar_arrive_expect_tx(bar, C::kStage);
-          tma_load_2d(dst, &P.tmap_w, bar, kb * 64, n0);
-          tma_load_2d(dst + C::kWBytes, &P.tmap_x, bar, kb * kW4K, tb);
-          if (!X8) tma_load_2d(dst + C::kWBytes + NT * 128, &P.tmap_x, bar, kb * kW4K + 64, tb);
+          if (wt) {
+            mbar_arrive_expect_tx(bar, C::kWBytes);
+            tma_load_2d(sbase + st.i * C::kWBytes, &P.tmap_w, bar, kb * 64, n0);
+          } else {
+            const uint32_t dst = sbase + kX0 + st.i * C::kXBytes;
+            mbar_arrive_expect_tx(bar, C::kXBytes);
+            tma_load_2d(dst, &P.tmap_x, bar, kb * kW4K, tb);
+            if (!X8) tma_load_2d(dst + NT * 128, &P.tmap_x, bar, kb * kW4K + 64, tb);
+          }
         }
         __syncwarp();
-        st.next(P.stages);
+        st.next(stages);
         ++issued;
       }
     }
     // after a wait that gave up: the copies still in flight
     if (!ok)
-      for (int i = max(0, issued - P.stages); i < issued; ++i)
-        role_wait(full0 + 8 * (i % P.stages), (i / P.stages) & 1);
-  } else if (warp > C::kMmaWarp + 1) {
-    if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
+      for (int i = max(0, issued - stages); i < issued; ++i)
+        role_wait(full0 + 8 * (i % stages), (i / stages) & 1);
   } else {
     if constexpr (C::kSplit) regs_dec<C::kRegsRest>();
     // =========================== MMA: group i of the CTA is warp i % 2's
     const int mw = warp - C::kMmaWarp;
     constexpr int kSteps = X8 ? 4 : 8;           // MMAs of a block
     constexpr int kPer = kSteps / C::kGroups;    // MMAs of a group
-    const uint64_t bd0 = make_sdesc(sbase + C::kWBytes, 128, 2);
+    const uint64_t bd0 = make_sdesc(sbase + kX0, 128, 2);
     const uint32_t idesc = P.idesc;
     RingPos st, ab, db;
     uint32_t blk = 0;
     for (int tile = first; tile < tiles && ok; tile += step) {
       for (int kb = kb0; kb < kb1 && ok; ++kb, ++blk) {
         if (C::kGroups > 1 || (blk & 1) == static_cast<uint32_t>(mw)) {
-          ok = role_wait(full0 + 8 * st.i, st.fill()) && role_wait(afull0 + 8 * ab.i, ab.fill());
+          ok = role_wait(xfull0 + 8 * st.i, st.fill()) && role_wait(afull0 + 8 * ab.i, ab.fill());
           // addresses in a descriptor are in units of 16 bytes
-          const uint64_t bd = bd0 + static_cast<uint32_t>(st.i * (C::kStage / 16));
+          const uint64_t bd = bd0 + static_cast<uint32_t>(st.i * (C::kXBytes / 16));
           const uint32_t at = abase + ab.i * C::kACols;
 #pragma unroll
           for (int j = 0; j < C::kGroups; ++j) {
@@ -571,7 +589,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
                 }
                 if (j + C::kMmaArrive >= C::kGroups) {  // this warp's last group of the block
                   tc_commit(aempty0 + 8 * ab.i);
-                  tc_commit(empty0 + 8 * st.i);
+                  tc_commit(xempty0 + 8 * st.i);
                 }
                 tc_commit(dfull0 + 8 * db.i);
               }
@@ -582,7 +600,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
         } else {
           db.next(C::kDBufs);
         }
-        st.next(P.stages);
+        st.next(C::kXStages);
         ab.next(C::kABufs);
       }
     }
