@@ -376,7 +376,15 @@ LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* resid
  *   w_scales [G, ld_s]     s, of `dtype`, G = ceil(K / group)
  *   w_zeros  [G, ld_s]     z, one byte each, its low four bits read; NULL: 8 everywhere
  *   out      [tok, ld_out] of `dtype`, written (lora_expand then adds the LoRA term).
- * Weights, and e4m3 values of x, are exact in the products; sums are fp32. */
+ * Weights, and e4m3 values of x, are exact in the products; sums are fp32.
+ * With up to 8 tokens bf16 values of x of 2^63 and more count as infinite, and
+ * products with |x| under 2^-57 lose bits.  A row of x that holds an infinity
+ * or a NaN gives values that are not finite, in that row alone.
+ * The outputs of a call depend on its sizes and strides and on the GPU, not on
+ * what else runs.  out must not overlap the inputs.
+ * x rows that are not 16-byte aligned, with more than 8 tokens, re-read W for
+ * every 16 tokens, and K is then limited by shared memory (about 98,000):
+ * LORA_ERR_UNSUPPORTED beyond, as for sizes from 2^28 (tok: 2^30) on. */
 LORA_API lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,
                                      const void* W, int64_t ld_w, const void* w_scales,
                                      const uint8_t* w_zeros, int64_t ld_s, void* out,

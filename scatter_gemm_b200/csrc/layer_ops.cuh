@@ -95,7 +95,7 @@ extern "C" lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* res
     return LORA_ERR_INVALID_ARGUMENT;
   if ((residual && (ld_res < H || ld_res_out < H)) || (out && ld_out < H) || (out_q && ld_q < H))
     return LORA_ERR_INVALID_ARGUMENT;
-  if (H > LORA_MAX_NORM_WIDTH) return LORA_ERR_UNSUPPORTED;
+  if (H > LORA_MAX_NORM_WIDTH || tok >= (1 << 30)) return LORA_ERR_UNSUPPORTED;
   if (tok == 0) return LORA_OK;
   if (!x || !weight) return LORA_ERR_INVALID_ARGUMENT;
   if (!aligned_to(x, 2) || !aligned_to(weight, 2) || !aligned_to(residual, 2) ||
@@ -204,7 +204,8 @@ extern "C" lora_status lora_rope_append(
   if (tok < 0 || head_dim < 1 || rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 2 ||
       axes < 1 || num_pages < 0 || page_size < 1 || !(eps >= 0.f))
     return LORA_ERR_INVALID_ARGUMENT;
-  if (head_dim > lora::kRopeMaxDim || axes > lora::kRopeMaxAxes) return LORA_ERR_UNSUPPORTED;
+  if (head_dim > lora::kRopeMaxDim || axes > lora::kRopeMaxAxes || tok >= (1 << 30))
+    return LORA_ERR_UNSUPPORTED;
   const int32_t* off = qkv_offsets;
   if (off[0] < 0 || off[1] < off[0] || off[2] < off[1] || off[3] < off[2] || off[3] > ld_qkv)
     return LORA_ERR_INVALID_ARGUMENT;
@@ -298,21 +299,23 @@ bool encode_w4(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint6
 constexpr int kW4Smem = 227 * 1024;
 constexpr int kMvSmem = 200 * 1024;
 
+// Shared memory of w4_mv for tt tokens: staged x and its sums, and two tiles' parts.
+template <int NT, int VW, int WARPS>
+int64_t w4_mv_bytes(int64_t tt, int K) {
+  const int64_t blocks = (K + 127) / 128;
+  return tt * lora::mv_row_bytes(static_cast<int>(blocks) * 128) + blocks * (4 / VW) * NT * 32 +
+         2 * WARPS * NT * 512;
+}
+
 template <class E, bool X8, int NT, int VW, int WARPS>
 lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
-  const int64_t blocks = (a.K + 127) / 128;
   const int tiles = (a.N + 15) / 16;
-  const int per_sm = WARPS == 8 ? LORA_MV_OCC : 1;
-  // staged x and sums of x for tt tokens, and two tiles' parts
   int tt = std::min(a.tok, 8 * NT);
-  auto bytes = [&]() {
-    return tt * static_cast<int64_t>(lora::mv_row_bytes(static_cast<int>(blocks) * 128)) +
-           blocks * (4 / VW) * NT * 32 + 2 * WARPS * NT * 512;
-  };
-  while (tt > 1 && bytes() > kMvSmem) --tt;
-  if (bytes() > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
-  int occ = per_sm;
-  const int smem = static_cast<int>(bytes());
+  while (tt > 1 && w4_mv_bytes<NT, VW, WARPS>(tt, a.K) > kMvSmem) --tt;
+  const int64_t bytes = w4_mv_bytes<NT, VW, WARPS>(tt, a.K);
+  if (bytes > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
+  const int smem = static_cast<int>(bytes);
+  int occ = WARPS == 8 ? 2 : 1;
   while (occ > 1 && occ * (smem + 1024) > 227 * 1024) --occ;
   const int64_t gy = (a.tok + tt - 1) / tt;
   if (gy > 65535) return LORA_ERR_UNSUPPORTED;
@@ -441,7 +444,10 @@ lora_status w4_project_group(const lora::W4Args& a, int sms, cudaStream_t st) {
   constexpr int VW = 1 << (GS - 5);
   const int64_t ldb = a.ld_x * (X8 ? 1 : 2);
   const bool tma_x = aligned_to(a.x, 16) && ldb % 16 == 0;
-  if (a.tok <= LORA_W4_MV_TOKENS || !tma_x)
+  // w4_mv reads the weights once for eight tokens at a time, so beyond that it
+  // only takes what TMA cannot; it needs all of K's x in shared memory.
+  const bool fits = w4_mv_bytes<1, VW, 8>(std::min(a.tok, 8), a.K) <= kMvSmem;
+  if ((a.tok <= LORA_W4_MV_TOKENS && fits) || !tma_x)
     return a.tok <= 8 ? w4_mv<E, X8, 1, VW, 8>(a, sms, st) : w4_mv<E, X8, 2, VW, 16>(a, sms, st);
   if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4, 4>(a, sms, st);
   if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4, 4>(a, sms, st);
@@ -470,6 +476,7 @@ extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float*
       ld_w < static_cast<int64_t>(K + 31) / 32 * 16)
     return LORA_ERR_INVALID_ARGUMENT;
   if ((x_scale != nullptr) != (x_dtype == LORA_E4M3)) return LORA_ERR_INVALID_ARGUMENT;
+  if (tok >= (1 << 30) || N > (1 << 28) || K > (1 << 28)) return LORA_ERR_UNSUPPORTED;
   if (tok == 0 || N == 0) return LORA_OK;
   if (!x || !W || !w_scales || !out) return LORA_ERR_INVALID_ARGUMENT;
   if ((x_dtype != LORA_E4M3 && !aligned_to(x, 2)) || !aligned_to(x_scale, 4) ||

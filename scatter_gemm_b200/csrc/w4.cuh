@@ -129,13 +129,7 @@ template <> struct MvScale<Fp16> {
   static constexpr float kX = 1.f, kOut = 0x1p24f;
 };
 
-#ifndef LORA_MV_OCC
-#define LORA_MV_OCC 2
-#endif
-#ifndef LORA_MV_DEPTH
-#define LORA_MV_DEPTH 4
-#endif
-constexpr int kMvDepth = LORA_MV_DEPTH;  // blocks of 128 K that a warp has in flight
+constexpr int kMvDepth = 4;  // blocks of 128 K that a warp has in flight
 
 // Bytes between the staged rows of x: a multiple of 128 plus 64, so that the
 // two tokens that a quarter of a warp reads lie in different banks.
@@ -172,7 +166,7 @@ struct MvBlock {
 //
 // grid = (runs of row tiles, token tiles of `tt` tokens).
 template <class E, bool X8, int NT, int VW, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? LORA_MV_OCC : 1)
+__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 2 : 1)
 w4_mv_kernel(const W4Args p, const int tt) {
   using C = typename std::conditional<X8, Fp16, E>::type;  // the operands' type
   extern __shared__ __align__(128) uint8_t mv_smem[];

@@ -465,3 +465,192 @@ def test_rope_offsets_beyond_32_bits():
     assert torch.equal(kc.view(-1, hkv, D)[slots], qkv[:, off[1]:off[2]].reshape(tok, hkv, D))
     assert torch.equal(vc.view(-1, hkv, D)[slots], qkv[:, off[2]:off[3]].reshape(tok, hkv, D))
     assert int(torch.count_nonzero(kc.view(-1, hkv * D).any(1))) == tok
+
+
+# ----------------------------------------------------------------------------
+# large K, paths, streams, and the operators one after the other
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tok", [1, 2, 8])
+def test_w4_long_rows(tok):
+    # x of 8 tokens does not fit shared memory: the tensor-core kernel takes it
+    check_w4(tok, tok, 65536 if tok == 1 else 40000, 48, "bf16", 128)
+    check_w4(tok, tok, 131072, 33, "fp16", 128, zeros=True)
+
+
+def test_w4_long_rows_off_the_16_byte_grid():
+    check_w4(5, 20, 30001, 40, "bf16", 64)
+    x = new(2, 120000, torch.bfloat16, pad=1)
+    out = new(2, 16, torch.bfloat16)
+    with pytest.raises(lora.LoraError) as e:
+        lora.lora_w4_project(x, torch.zeros(16, 60000, dtype=torch.uint8, device="cuda"),
+                             torch.zeros(938, 16, dtype=torch.bfloat16, device="cuda"), out,
+                             group_size=128)
+    assert e.value.status == lora.LORA_ERR_UNSUPPORTED
+    assert (out == SENT).all()
+
+
+def test_w4_paths_and_launches():
+    for tok, N, want, launches in ((8, 512, lora.PATH_GENERAL, 1), (9, 19000, lora.PATH_TENSOR, 1),
+                                   (9, 512, lora.PATH_TENSOR | lora.PATH_SPLITK, 1),
+                                   # 150 tiles on 148 SMs: a round and two tiles left over
+                                   (128, 150 * 128, lora.PATH_TENSOR | lora.PATH_SPLITK, 2)):
+        x, sx, q, packed, s, z = w4_inputs(tok, tok, 256, N, "bf16", 128, False, False)
+        out = torch.empty(tok, N, dtype=x.dtype, device="cuda")
+        lora.reset_launch_count()
+        lora.lora_w4_project(x, packed, s, out, group_size=128)
+        if torch.cuda.get_device_properties(0).multi_processor_count == 148:
+            assert lora.last_path() == want and lora.launch_count() == launches, (tok, N)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+def test_w4_tiles_left_over(group):
+    # whole rounds of tiles and a few more, rows and tokens ragged
+    check_w4(6, 130, 640, 75 * 128 + 5, "bf16", group, True)
+    check_w4(7, 200, 384, 80 * 128 - 3, "fp16", group, False, x8=True)
+
+
+def test_on_another_stream():
+    g = gen(40)
+    x, res = rand(g, 30, 512, dtype=torch.bfloat16), rand(g, 30, 512, dtype=torch.bfloat16)
+    w = rand(g, 512, dtype=torch.bfloat16)
+    want = torch.empty_like(x)
+    lora.lora_rmsnorm(x, w, want, residual=res.clone())
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got, r2 = torch.empty_like(x), res.clone()
+    torch.cuda.synchronize()
+    lora.lora_rmsnorm(x, w, got, residual=r2, stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+    with torch.cuda.stream(st):  # the current stream is the default
+        got2 = torch.empty_like(x)
+        lora.lora_rmsnorm(x, w, got2, residual=res.clone())
+    st.synchronize()
+    assert torch.equal(got2, want)
+
+
+def test_two_streams_at_once():
+    # kernels that take tensor memory and clusters, from two streams, many times
+    jobs = []
+    for tok, K, N, x8 in ((40, 2048, 1024, False), (130, 1024, 19500, True)):
+        x, sx, q, packed, s, z = w4_inputs(tok, tok, K, N, "bf16", 128, False, x8)
+        want = torch.empty(tok, N, dtype=torch.bfloat16, device="cuda")
+        lora.lora_w4_project(x, packed, s, want, group_size=128, x_scale=sx)
+        jobs.append((x, packed, s, sx, want, [torch.empty_like(want) for _ in range(20)],
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x, packed, s, sx, want, outs, st in jobs:
+            lora.lora_w4_project(x, packed, s, outs[i], group_size=128, x_scale=sx, stream=st)
+    torch.cuda.synchronize()
+    for x, packed, s, sx, want, outs, st in jobs:
+        assert all(torch.equal(o, want) for o in outs)
+    assert lora.device_error() == 0
+
+
+class Step:
+    """The attention input of one decoder layer for a batch of adapted requests:
+    norm, 4-bit projection of its 8-bit output, LoRA pair on its 16-bit output,
+    rotation and append."""
+
+    def __init__(self, seed, tok, hidden=1024, hq=8, hkv=2, D=128, rank=16, adapters=4, big=False):
+        g = gen(seed)
+        dt = torch.bfloat16
+        self.off = [0, hq * D, (hq + hkv) * D, (hq + 2 * hkv) * D]
+        N = self.off[3]
+        self.D, self.rank = D, rank
+        self.x, self.res = rand(g, tok, hidden, dtype=dt), rand(g, tok, hidden, dtype=dt)
+        self.w = (1 + rand(g, hidden, std=0.2)).to(dt)
+        W = rand(g, N, hidden, dtype=dt, std=hidden ** -0.5)
+        self.packed, self.s, self.z = lora.w4_quantize(W, 128, zeros=True)
+        self.A = rand(g, adapters, 3 * rank, hidden, dtype=dt, std=0.02)
+        self.B = rand(g, adapters, N, rank, dtype=dt, std=0.02)
+        cut = sorted(torch.randint(0, tok + 1, (adapters - 1,), generator=g, device="cuda").tolist())
+        self.si = torch.tensor([0] + cut + [tok], dtype=torch.int32, device="cuda")
+        self.wi = torch.arange(adapters, dtype=torch.int32, device="cuda").flip(0).contiguous()
+        self.pm = torch.randperm(tok, generator=g, device="cuda").to(torch.int32)
+        self.sc = torch.tensor([2.0, 0.5, 0.0, 1.0], device="cuda")[:adapters].contiguous()
+        self.cs = rand(g, 300, D).clamp(-1, 1)
+        self.pos = torch.randint(0, 300, (tok,), generator=g, device="cuda")
+        self.slots = torch.randperm(4 * 64, generator=g, device="cuda")[:tok]
+        self.kc, self.vc = (torch.zeros(4, 64, hkv, D, dtype=dt, device="cuda") for _ in range(2))
+        self.qw, self.kw = rand(g, D, dtype=dt), rand(g, D, dtype=dt)
+        self.out = torch.empty_like(self.x)
+        self.q8 = torch.empty(tok, hidden, dtype=E4M3, device="cuda")
+        self.sx = torch.empty(tok, device="cuda")
+        self.r = torch.empty(tok, 3 * rank, dtype=dt, device="cuda")
+        self.qkv = torch.empty(tok, N, dtype=dt, device="cuda")
+        self.q = torch.empty(tok, self.off[1], dtype=dt, device="cuda")
+
+    def run(self):
+        lora.lora_rmsnorm(self.x, self.w, self.out, residual=self.res, out_q=self.q8,
+                          out_scale=self.sx)
+        lora.lora_w4_project(self.q8, self.packed, self.s, self.qkv, group_size=128,
+                             w_zeros=self.z, x_scale=self.sx)
+        lora.lora_shrink_expand(self.out, self.A, self.B, self.si, self.wi, self.pm, self.off,
+                                self.sc, self.r, self.qkv)
+        lora.lora_rope_append(self.qkv, self.off, self.D, self.pos, self.cs, self.kc, self.vc,
+                              self.slots, q_out=self.q, q_weight=self.qw, k_weight=self.kw)
+
+
+@pytest.mark.parametrize("tok", [1, 7, 50, 200])
+def test_a_layer_of_them(tok):
+    s = Step(tok, tok)
+    x0, r0 = s.x.clone(), s.res.clone()
+    s.run()
+    torch.cuda.synchronize()
+    h = (x0.float() + r0.float()).bfloat16()
+    assert torch.equal(s.res, h) and torch.equal(s.x, x0)
+    v = h.double() * torch.rsqrt(h.double().pow(2).mean(1, keepdim=True) + 1e-6) * s.w.double()
+    within(s.out, v, v.abs() * (2.0 ** -8 + 2.0 ** -17), "x")
+    # from what each operator was given: the projection, then the LoRA term
+    of = torch.arange(v.shape[1], device="cuda") // 128
+    q = lora.w4_unpack(s.packed, v.shape[1]).double()
+    W = (q - s.z.double()[of].T) * s.s.double()[of].T
+    x8 = s.q8.double() * s.sx.double()[:, None]
+    base = x8 @ W.T
+    R = s.rank
+    lo = torch.zeros_like(base)
+    si = s.si.tolist()
+    for g_, a in enumerate(s.wi.tolist()):
+        rows = s.pm[si[g_]:si[g_ + 1]].long()
+        ra = s.out[rows].double() @ s.A[a].double().T
+        for t in range(3):
+            c0, c1 = s.off[t], s.off[t + 1]
+            lo[rows, c0:c1] = float(s.sc[a]) * ra[:, t * R:(t + 1) * R] @ s.B[a, c0:c1].double().T
+    # the projection rounded, the rank activations rounded, their sum rounded
+    ref = base + lo
+    tol = (base.abs() + ref.abs()) * 2.0 ** -8 + 2e-2 * lo.abs() + 2.0 ** -8
+    within(s.qkv, ref, tol, "q/k/v")
+    qr, kr, vr, mq, mk = rope_ref(s.qkv, s.off, s.D, s.pos, s.cs, s.D, None, False, s.qw, s.kw, 1e-6, 0.0)
+    within(s.q.reshape(qr.shape), qr, qr.abs() * 2.0 ** -8 + mq * 2.0 ** -17, "q")
+    at = s.slots
+    hkv = s.kc.shape[2]
+    within(s.kc.view(-1, hkv, s.D)[at], kr, kr.abs() * 2.0 ** -8 + mk * 2.0 ** -17, "k")
+    assert torch.equal(s.vc.view(-1, hkv, s.D)[at].double(), vr)
+    # x in 8 bits is near x: half a step of e4m3 in 448 steps' range of a row
+    assert (x8 - v).abs().le(v.abs() * 2.0 ** -4 + 2.0 ** -10 * s.sx.double()[:, None] +
+                             v.abs() * 2.0 ** -15).all()
+
+
+@pytest.mark.parametrize("tok", [3, 60])
+def test_a_layer_of_them_in_a_graph(tok):
+    s, t = Step(70 + tok, tok), Step(80 + tok, tok)
+    s.run()  # first calls of each kernel outside of the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.run()
+    # the other step's inputs in the first one's buffers
+    for n in ("x", "res", "w", "packed", "s", "z", "A", "B", "si", "wi", "pm", "sc", "cs", "pos",
+              "slots", "qw", "kw"):
+        getattr(s, n).copy_(getattr(t, n))
+    s.kc.zero_(), s.vc.zero_()
+    graph.replay()
+    t.run()
+    torch.cuda.synchronize()
+    for n in ("res", "out", "sx", "qkv", "q", "kc", "vc"):
+        assert torch.equal(getattr(s, n), getattr(t, n)), n
+    assert torch.equal(s.q8.view(torch.uint8), t.q8.view(torch.uint8))
+    assert lora.device_error() == 0
