@@ -427,6 +427,17 @@ LORA_API lora_status lora_rope_append(
     int64_t num_pages, int page_size, lora_dtype cache_dtype, float k_scale, float v_scale,
     const void* slots, int index_bytes, int tok, lora_dtype dtype, void* stream);
 
+/* The three operators with their arguments in one array, for callers to whom
+ * every argument of a foreign call costs (an interpreter's binding): 64-bit
+ * words in the order of the parameters above, integers and pointers as int64_t
+ * and floats as double, the stream last.  A host array stands by value in the
+ * place of its pointer: four words for qkv_offsets, three for the strides of
+ * each cache; axis_map is one word, 0 or 1, and its rotary_dim/2 bytes follow
+ * the last word.  Arguments, errors and results are those of the operator. */
+LORA_API lora_status lora_rmsnorm_packed(const void* words);
+LORA_API lora_status lora_w4_project_packed(const void* words);
+LORA_API lora_status lora_rope_append_packed(const void* words);
+
 /* ---- 64-bit index tables ------------------------------------------------
  * lora_shrink_i64 / lora_expand_i64 take seg_indptr, weight_indices and
  * permutation as int64_t (the default index type of PyTorch), as the

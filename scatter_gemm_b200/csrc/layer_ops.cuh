@@ -497,3 +497,118 @@ extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float*
   return x8 ? w4_project<lora::Fp16, true>(a, dev->sms, st)
             : w4_project<lora::Fp16, false>(a, dev->sms, st);
 }
+
+// ------------------------------------------------------------------ packed arguments
+
+namespace {
+
+// Takes the words of a packed call in their order.
+class Words {
+ public:
+  explicit Words(const void* p) : p_(static_cast<const char*>(p)) {}
+  int64_t i64() { return take<int64_t>(); }
+  int i32() {
+    // out of range for an int parameter: as invalid as it is there
+    const int64_t v = i64();
+    return v < INT32_MIN || v > INT32_MAX ? -1 : static_cast<int>(v);
+  }
+  float f32() { return static_cast<float>(take<double>()); }
+  lora_dtype dtype() { return static_cast<lora_dtype>(i32()); }
+  template <class T = void>
+  T* ptr() {
+    return reinterpret_cast<T*>(static_cast<uintptr_t>(i64()));
+  }
+  const void* rest() const { return p_; }
+
+ private:
+  template <class T>
+  T take() {
+    T v;
+    std::memcpy(&v, p_, sizeof(v));
+    p_ += 8;
+    return v;
+  }
+  const char* p_;
+};
+
+}  // namespace
+
+extern "C" lora_status lora_rmsnorm_packed(const void* words) {
+  if (!words) return LORA_ERR_INVALID_ARGUMENT;
+  Words w(words);
+  const void* x = w.ptr();
+  const int64_t ld_x = w.i64();
+  const void* res = w.ptr();
+  const int64_t ld_res = w.i64();
+  void* res_out = w.ptr();
+  const int64_t ld_res_out = w.i64();
+  const void* weight = w.ptr();
+  const float w0 = w.f32(), eps = w.f32();
+  void* out = w.ptr();
+  const int64_t ld_out = w.i64();
+  void* q = w.ptr();
+  const int64_t ld_q = w.i64();
+  float* scale = w.ptr<float>();
+  const int tok = w.i32(), H = w.i32();
+  const lora_dtype dt = w.dtype();
+  return lora_rmsnorm(x, ld_x, res, ld_res, res_out, ld_res_out, weight, w0, eps, out, ld_out, q,
+                      ld_q, scale, tok, H, dt, w.ptr());
+}
+
+extern "C" lora_status lora_w4_project_packed(const void* words) {
+  if (!words) return LORA_ERR_INVALID_ARGUMENT;
+  Words w(words);
+  const void* x = w.ptr();
+  const int64_t ld_x = w.i64();
+  const float* x_scale = w.ptr<float>();
+  const void* W = w.ptr();
+  const int64_t ld_w = w.i64();
+  const void* s = w.ptr();
+  const uint8_t* z = w.ptr<uint8_t>();
+  const int64_t ld_s = w.i64();
+  void* out = w.ptr();
+  const int64_t ld_out = w.i64();
+  const int tok = w.i32(), K = w.i32(), N = w.i32(), group = w.i32();
+  const lora_dtype x_dt = w.dtype(), dt = w.dtype();
+  return lora_w4_project(x, ld_x, x_scale, W, ld_w, s, z, ld_s, out, ld_out, tok, K, N, group,
+                         x_dt, dt, w.ptr());
+}
+
+extern "C" lora_status lora_rope_append_packed(const void* words) {
+  if (!words) return LORA_ERR_INVALID_ARGUMENT;
+  Words w(words);
+  const void* qkv = w.ptr();
+  const int64_t ld_qkv = w.i64();
+  int32_t off[4];
+  for (int32_t& o : off) o = w.i32();
+  const int D = w.i32(), R = w.i32();
+  const void* pos = w.ptr();
+  const int64_t ld_pos = w.i64();
+  const int axes = w.i32();
+  const bool map = w.i64() != 0;
+  const float* cs = w.ptr<float>();
+  const int64_t max_pos = w.i64();
+  const int inter = w.i32();
+  const void* qw = w.ptr();
+  const void* kw = w.ptr();
+  const float w0 = w.f32(), eps = w.f32();
+  void* q_out = w.ptr();
+  const int64_t ld_q = w.i64();
+  void* kc = w.ptr();
+  int64_t ks[3], vs[3];
+  for (int64_t& v : ks) v = w.i64();
+  void* vc = w.ptr();
+  for (int64_t& v : vs) v = w.i64();
+  const int64_t pages = w.i64();
+  const int page = w.i32();
+  const lora_dtype cdt = w.dtype();
+  const float k_scale = w.f32(), v_scale = w.f32();
+  const void* slots = w.ptr();
+  const int ib = w.i32(), tok = w.i32();
+  const lora_dtype dt = w.dtype();
+  void* stream = w.ptr();
+  return lora_rope_append(qkv, ld_qkv, off, D, R, pos, ld_pos, axes,
+                          map ? static_cast<const uint8_t*>(w.rest()) : nullptr, cs, max_pos,
+                          inter, qw, kw, w0, eps, q_out, ld_q, kc, ks, vc, vs, pages, page, cdt,
+                          k_scale, v_scale, slots, ib, tok, dt, stream);
+}

@@ -88,6 +88,10 @@ def lib() -> ctypes.CDLL:
                                            _F, _F, _P, _L, _P, _P, _P, _P, _L, _I, _I, _F, _F, _P,
                                            _I, _I, _I, _P]
             l.lora_rope_append.restype = _I
+            for name in ("lora_rmsnorm", "lora_w4_project", "lora_rope_append"):
+                f = getattr(l, name + "_packed")
+                f.argtypes = [ctypes.c_char_p]
+                f.restype = _I
             _lib = l
     return _lib
 
@@ -460,21 +464,30 @@ def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> i
     return t.data_ptr()
 
 
-def _call_on(dev: int, name: str, args, stream) -> None:
-    """Calls an entry point with the tensors' device current, on the given
+# The words of the packed entry points: q an integer or an address, d a float.
+_WORDS = {
+    "lora_rmsnorm": struct.Struct("=7q2d9q").pack,
+    "lora_w4_project": struct.Struct("=17q").pack,
+    "lora_rope_append": struct.Struct("=17q2d13q2d5q").pack,
+}
+
+
+def _call_on(dev: int, name: str, args, stream, tail: bytes = b"") -> None:
+    """Calls a packed entry point with the tensors' device current, on the given
     stream or that device's current one."""
     if dev < 0:
         raise ValueError(f"{name} needs CUDA tensors")
-    fn = getattr(_lib or lib(), name)
+    fn = getattr(_lib or lib(), name + "_packed")
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
         raw = _stream(stream)
+    words = _WORDS[name](*args, raw) + tail
     if dev == torch._C._cuda_getDevice():
-        st = fn(*args, raw)
+        st = fn(words)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, raw)
+            st = fn(words)
     if st != LORA_OK:
         raise LoraError(name, st)
 
@@ -499,7 +512,7 @@ def lora_rmsnorm(x: torch.Tensor, weight: torch.Tensor, out: Optional[torch.Tens
     dtype, dev = x.dtype, x.get_device()
     ld_x = _ld(x, "x", dtype, shape, dev)
     w = _flat(weight, "weight", dtype, H, dev)
-    ptr_r = ptr_ro = ptr_o = ptr_q = ptr_s = None
+    ptr_r = ptr_ro = ptr_o = ptr_q = ptr_s = 0
     ld_r = ld_ro = ld_o = ld_q = 0
     if residual is not None:
         ld_ro = ld_r = _ld(residual, "residual", dtype, shape, dev)
@@ -559,7 +572,7 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     ld_s = _ld(w_scales, "w_scales", dtype, s_shape, dev)
     if w_scales.shape != s_shape:
         raise ValueError(f"w_scales must be {s_shape}, got {tuple(w_scales.shape)}")
-    ptr_z = ptr_sx = None
+    ptr_z = ptr_sx = 0
     if w_zeros is not None:
         if _ld(w_zeros, "w_zeros", torch.uint8, s_shape, dev) != ld_s or w_zeros.shape != s_shape:
             raise ValueError("w_zeros must have the shape and row stride of w_scales")
@@ -651,12 +664,9 @@ def rope_axis_map(sections: Sequence[int], interleaved: bool = False) -> list:
     return [i % m if i < m * sec[i % m] else 0 for i in range(sum(sec))]
 
 
-_PACK4, _PACK3 = struct.Struct("=4i").pack, struct.Struct("=3q").pack
-
-
-def _cache(t: torch.Tensor, name: str, hkv: int, D: int, dev: int) -> bytes:
+def _cache(t: torch.Tensor, name: str, hkv: int, D: int, dev: int):
     """Checks a [pages, page_size, Hkv, D] cache of any strides but the last;
-    returns the others as C integers."""
+    returns the others."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the other tensors, got {t.device}")
     shape = t.shape
@@ -665,7 +675,7 @@ def _cache(t: torch.Tensor, name: str, hkv: int, D: int, dev: int) -> bytes:
     page, slot, head, inner = t.stride()
     if inner != 1 and D > 1:
         raise ValueError(f"{name} must have a unit inner stride")
-    return _PACK3(page, slot, head)
+    return page, slot, head
 
 
 def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: int,
@@ -715,7 +725,7 @@ def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: 
     max_pos, R = table
     if R > D or R % 2 or (R and max_pos < 1):
         raise ValueError("cos_sin must have 2 * frequencies <= head_dim columns and a row")
-    axes, ld_pos, amap = 1, 0, None
+    axes, ld_pos, amap = 1, 0, b""
     if positions.dim() == 1:
         ptr_p = _flat(positions, "positions", idt, tok, dev)
         if axis_map is not None:
@@ -733,8 +743,8 @@ def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: 
         elif axes > 1:
             raise ValueError("positions of several axes need an axis_map")
     hkv = (o2 - o1) // D
-    ks = _cache(k_cache, "k_cache", hkv, D, dev)
-    vs = _cache(v_cache, "v_cache", hkv, D, dev)
+    kp, kl, kh = _cache(k_cache, "k_cache", hkv, D, dev)
+    vp, vl, vh = _cache(v_cache, "v_cache", hkv, D, dev)
     c_shape, c_dtype = k_cache.shape, k_cache.dtype
     if c_shape != v_cache.shape or c_dtype is not v_cache.dtype:
         raise ValueError("k_cache and v_cache must share shape and element type")
@@ -746,17 +756,18 @@ def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: 
     ld_q = _ld(q_out, "q_out", dtype, (tok, o1 - o0), dev)
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
-    qw = kw = None
+    qw = kw = 0
     if q_weight is not None:
         qw = _flat(q_weight, "q_weight", dtype, D, dev)
         kw = _flat(k_weight, "k_weight", dtype, D, dev)
     if tok:
         _call_on(dev, "lora_rope_append",
-                 (qkv.data_ptr(), ld, _PACK4(o0, o1, o2, o3), D, R, ptr_p, ld_pos, axes, amap,
-                  cos_sin.data_ptr(), max_pos, interleaved, qw, kw, weight_offset, eps,
-                  q_out.data_ptr(), ld_q, k_cache.data_ptr(), ks, v_cache.data_ptr(), vs,
-                  c_shape[0] if c_shape[1] else 0, c_shape[1] or 1, c_dt, k_scale, v_scale,
-                  ptr_s, 8 if idt is torch.int64 else 4, tok, dt), stream)
+                 (qkv.data_ptr(), ld, o0, o1, o2, o3, D, R, ptr_p, ld_pos, axes, 1 if amap else 0,
+                  cos_sin.data_ptr(), max_pos, 1 if interleaved else 0, qw, kw, weight_offset,
+                  eps, q_out.data_ptr(), ld_q, k_cache.data_ptr(), kp, kl, kh,
+                  v_cache.data_ptr(), vp, vl, vh, c_shape[0] if c_shape[1] else 0,
+                  c_shape[1] or 1, c_dt, k_scale, v_scale, ptr_s,
+                  8 if idt is torch.int64 else 4, tok, dt), stream, amap)
     return q_out
 
 

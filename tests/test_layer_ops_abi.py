@@ -227,3 +227,33 @@ def test_rope_axis_map():
     for bad in ([], [1] * 5, [2, -1]):
         with pytest.raises(ValueError):
             lora.rope_axis_map(bad)
+
+
+def test_packed_calls_give_what_the_calls_give(L):
+    assert L.lora_rmsnorm_packed(None) == L.lora_w4_project_packed(None) == INVALID
+    assert L.lora_rope_append_packed(None) == INVALID
+    n = lambda **k: L.lora_rmsnorm_packed(lora._WORDS["lora_rmsnorm"](*{**dict(
+        x=P, ld_x=64, res=P, ld_res=64, ro=P, ld_ro=64, w=P, w0=0.0, eps=1e-6, out=P, ld_out=64,
+        q=P, ld_q=64, sc=P, tok=0, H=64, dt=0, st=0), **k}.values()))
+    for kw, want in ((dict(), OK), (dict(dt=2), UNSUPPORTED), (dict(eps=-1.0), INVALID),
+                     (dict(res=0), INVALID), (dict(sc=0), INVALID), (dict(ld_q=63), INVALID),
+                     (dict(tok=1 << 40), INVALID)):
+        assert n(**kw) == want, kw
+    w = lambda **k: L.lora_w4_project_packed(lora._WORDS["lora_w4_project"](*{**dict(
+        x=P, ld_x=128, sx=0, W=P, ld_w=64, s=P, z=P, ld_s=16, out=P, ld_out=16, tok=0, K=128, N=16,
+        group=128, xdt=0, dt=0, st=0), **k}.values()))
+    for kw, want in ((dict(), OK), (dict(xdt=2), INVALID), (dict(group=16), UNSUPPORTED),
+                     (dict(ld_out=15), INVALID), (dict(tok=3, W=P + 8), UNSUPPORTED)):
+        assert w(**kw) == want, kw
+    r = lambda tail=b"", **k: L.lora_rope_append_packed(lora._WORDS["lora_rope_append"](*{**dict(
+        qkv=P, ld=512, o0=0, o1=256, o2=384, o3=512, D=64, R=64, pos=P, ld_pos=8, axes=1, amap=0,
+        cs=P, max_pos=10, inter=0, qw=0, kw=0, w0=0.0, eps=1e-6, q=P, ld_q=256, kc=P, k0=1024,
+        k1=128, k2=64, vc=P, v0=1024, v1=128, v2=64, pages=4, page=8, cdt=0, ksc=1.0, vsc=1.0,
+        slots=P, ib=8, tok=0, dt=0, st=0), **k}.values()) + tail)
+    for tail, kw, want in ((b"", dict(), OK), (b"", dict(o3=500), INVALID), (b"", dict(k1=-1), INVALID),
+                           (b"", dict(v2=-1), INVALID), (b"", dict(axes=2), INVALID),
+                           (bytes([0, 1] * 16), dict(axes=2, amap=1), OK),
+                           (bytes([0, 2] * 16), dict(axes=2, amap=1), INVALID),
+                           (b"", dict(vsc=0.0), INVALID), (b"", dict(page=0), INVALID),
+                           (b"", dict(cdt=1), UNSUPPORTED), (b"", dict(ib=2), UNSUPPORTED)):
+        assert r(tail, **kw) == want, kw
