@@ -12,10 +12,6 @@
 #include <initializer_list>
 #include <type_traits>
 
-#ifndef LORA_W4_MV_TOKENS
-#define LORA_W4_MV_TOKENS 8  // 4-bit projection: tokens up to which w4_mv runs
-#endif
-
 namespace {
 
 // Lets a kernel take up to `bytes` of dynamic shared memory, once for each
@@ -300,30 +296,28 @@ constexpr int kW4Smem = 227 * 1024;
 constexpr int kMvSmem = 200 * 1024;
 
 // Shared memory of w4_mv for tt tokens: staged x and its sums, and two tiles' parts.
-template <int NT, int VW, int WARPS>
+template <int NT, int VW>
 int64_t w4_mv_bytes(int64_t tt, int K) {
   const int64_t blocks = (K + 127) / 128;
   return tt * lora::mv_row_bytes(static_cast<int>(blocks) * 128) + blocks * (4 / VW) * NT * 32 +
-         2 * WARPS * NT * 512;
+         2 * lora::kMvWarps * NT * 512;
 }
 
-template <class E, bool X8, int NT, int VW, int WARPS>
+template <class E, bool X8, int NT, int VW>
 lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
   const int tiles = (a.N + 15) / 16;
   int tt = std::min(a.tok, 8 * NT);
-  while (tt > 1 && w4_mv_bytes<NT, VW, WARPS>(tt, a.K) > kMvSmem) --tt;
-  const int64_t bytes = w4_mv_bytes<NT, VW, WARPS>(tt, a.K);
+  while (tt > 1 && w4_mv_bytes<NT, VW>(tt, a.K) > kMvSmem) --tt;
+  const int64_t bytes = w4_mv_bytes<NT, VW>(tt, a.K);
   if (bytes > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
   const int smem = static_cast<int>(bytes);
-  int occ = WARPS == 8 ? 2 : 1;
-  while (occ > 1 && occ * (smem + 1024) > 227 * 1024) --occ;
   const int64_t gy = (a.tok + tt - 1) / tt;
   if (gy > 65535) return LORA_ERR_UNSUPPORTED;
-  const dim3 grid(std::min(tiles, sms * occ), static_cast<unsigned>(gy));
-  auto kernel = lora::w4_mv_kernel<E, X8, NT, VW, WARPS>;
+  const dim3 grid(std::min(tiles, sms), static_cast<unsigned>(gy));
+  auto kernel = lora::w4_mv_kernel<E, X8, NT, VW>;
   static std::atomic<uint64_t> ready{0};  // a bit for each device
   if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kMvSmem)) return LORA_ERR_CUDA;
-  kernel<<<grid, 32 * WARPS, smem, st>>>(a, tt);
+  kernel<<<grid, lora::kMvThreads, smem, st>>>(a, tt);
   ++g_launches;
   g_last_path = LORA_PATH_GENERAL;
   return launch_status();
@@ -444,11 +438,13 @@ lora_status w4_project_group(const lora::W4Args& a, int sms, cudaStream_t st) {
   constexpr int VW = 1 << (GS - 5);
   const int64_t ldb = a.ld_x * (X8 ? 1 : 2);
   const bool tma_x = aligned_to(a.x, 16) && ldb % 16 == 0;
-  // w4_mv reads the weights once for eight tokens at a time, so beyond that it
-  // only takes what TMA cannot; it needs all of K's x in shared memory.
-  const bool fits = w4_mv_bytes<1, VW, 8>(std::min(a.tok, 8), a.K) <= kMvSmem;
-  if ((a.tok <= LORA_W4_MV_TOKENS && fits) || !tma_x)
-    return a.tok <= 8 ? w4_mv<E, X8, 1, VW, 8>(a, sms, st) : w4_mv<E, X8, 2, VW, 16>(a, sms, st);
+  // w4_mv reads the weights once for eight tokens at a time (8 tokens at 4096 x
+  // 24576: 21 us, against 28 with w4_tc; 9 at 4096 x 6144: 12.6 against 11.5),
+  // so beyond that it only takes what TMA cannot; it needs all of K's x in
+  // shared memory.
+  const bool fits = w4_mv_bytes<1, VW>(std::min(a.tok, 8), a.K) <= kMvSmem;
+  if ((a.tok <= 8 && fits) || !tma_x)
+    return a.tok <= 8 ? w4_mv<E, X8, 1, VW>(a, sms, st) : w4_mv<E, X8, 2, VW>(a, sms, st);
   if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4, 4>(a, sms, st);
   if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4, 4>(a, sms, st);
   if (a.tok <= 64) return w4_tc<E, X8, 64, GS, 4, 8>(a, sms, st);

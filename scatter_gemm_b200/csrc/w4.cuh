@@ -73,6 +73,9 @@ __device__ __forceinline__ uint2 w4_from_e4m3(uint32_t b) {
                                                     __NV_E4M3);
   const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(b >> 16),
                                                     __NV_E4M3);
+  if constexpr (std::is_same<E, Fp16>::value)
+    return make_uint2(lo.x | (static_cast<uint32_t>(lo.y) << 16),
+                      hi.x | (static_cast<uint32_t>(hi.y) << 16));
   const float2 f = __half22float2(__half2(lo)), g = __half22float2(__half2(hi));
   return make_uint2(E::f2_to_u32(f.x, f.y), E::f2_to_u32(g.x, g.y));
 }
@@ -130,6 +133,7 @@ template <> struct MvScale<Fp16> {
 };
 
 constexpr int kMvDepth = 4;  // blocks of 128 K that a warp has in flight
+constexpr int kMvWarps = 16, kMvThreads = 32 * kMvWarps;
 
 // Bytes between the staged rows of x: a multiple of 128 plus 64, so that the
 // two tokens that a quarter of a warp reads lie in different banks.
@@ -164,14 +168,22 @@ struct MvBlock {
 // neighbouring pieces of the same rows.  At the end of a tile the warps' parts
 // meet in shared memory and are added in the warps' order.
 //
+// One block of 16 warps an SM, as two of 8 would stage x twice: 20.6 against
+// 22.6 us for 8 tokens (7.7 against 8.5 us for one token at 4096 x 6144).  At
+// 4096 x 24576 one token takes 19 us, 2.7 TB/s, where the weights' 52 MB alone
+// would take 8: about 5 us are start-up and end, and then the bound is what
+// four warps a scheduler issue, some 170 instructions for each KB of weights.
+// Weights by 8, 16 or 32 rows a warp, deeper prefetch, or three and four
+// smaller blocks an SM were all within 5 % of this.
+//
 // grid = (runs of row tiles, token tiles of `tt` tokens).
-template <class E, bool X8, int NT, int VW, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == 8 ? 2 : 1)
+template <class E, bool X8, int NT, int VW>
+__global__ void __launch_bounds__(kMvThreads, 1)
 w4_mv_kernel(const W4Args p, const int tt) {
   using C = typename std::conditional<X8, Fp16, E>::type;  // the operands' type
   extern __shared__ __align__(128) uint8_t mv_smem[];
   constexpr int kSub = 4 / VW;  // groups of a block
-  constexpr int kThreads = 32 * WARPS;
+  constexpr int WARPS = kMvWarps, kThreads = kMvThreads;
   constexpr int kPart = NT * 128;  // sums of a tile
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
