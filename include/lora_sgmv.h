@@ -41,10 +41,11 @@
  *    default stream) and return.  The library allocates no device memory and
  *    keeps no state between calls; calls may be made from several host
  *    threads and on several streams at once.  Kernels of calls that overlap on
- *    the GPU never wait for each other: every kernel that holds tensor memory
+ *    the GPU never wait for each other: a kernel that holds tensor memory
  *    (TMEM) takes at most 256 of an SM's 512 columns and enough shared memory
- *    that at most two of its thread blocks share an SM.  The exception is other
- *    software's kernels: a kernel outside this library that holds more TMEM
+ *    that at most two of its thread blocks share an SM, or all 512 and enough
+ *    shared memory that no other such block fits beside it.  The exception is
+ *    other software's kernels: a kernel outside this library that holds TMEM
  *    on an SM while it waits for thread blocks elsewhere can make a thread
  *    block of this library wait for its TMEM; do not overlap such kernels with
  *    these calls.
@@ -61,6 +62,8 @@
  *    lora_shrink / lora_expand, as on the pages (section "Behaviour changes");
  *    lora_validate checks them.  Every index a kernel reads is clamped to its
  *    tensor, so bad tables give wrong values, never an out-of-bounds access.
+ *  - lora_w4_project may put its last tiles into a second kernel, which starts
+ *    while the first one still runs and ends after it.
  *  - Errors in the ARGUMENTS (null pointers, sizes, strides, dtype) are
  *    reported before anything is enqueued.
  */

@@ -387,13 +387,13 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
     return LORA_ERR_CUDA;
   const int* most = cluster_counts(kernel, C::kThreads, smem);
   if (!most) return LORA_ERR_CUDA;
-  // Whole rounds of one tile for each SM; the tiles left over share the SMs by
+  // Whole waves of one tile for each SM; the tiles left over share the SMs by
   // splitting their K range over clusters, in a launch of their own that takes
   // SMs as the first one's blocks leave them.
   auto launch = [&](int64_t lo, int64_t hi, bool after) {
     P.tile0 = static_cast<int>(lo);
     P.tile1 = static_cast<int>(hi);
-    // Least rounds x (blocks of K each + 4): a round's set-up and the adding up
+    // Least waves x (blocks of K each + 4): a wave's set-up and the adding up
     // of the parts cost about as much as four blocks.
     P.cs = 1;
     if (hi - lo < sms) {
@@ -423,7 +423,7 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
     return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
   };
   const int64_t left = tiles % sms;
-  // (Up to 64 tokens a second round of whole tiles, which has the memory to
+  // (Up to 64 tokens a second wave of whole tiles, which has the memory to
   // itself, is the shorter: 31.7 against 33.7 us at 32 tokens x 4096 x 24576.)
   const bool split = NT > 64 && tiles > sms && left > 0 && left <= sms / 2 && P.nkb > 1;
   const int64_t whole = split ? tiles - left : tiles;

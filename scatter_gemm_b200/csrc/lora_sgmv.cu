@@ -14,6 +14,7 @@
 //   With a workspace, more segments than adapters and at least 64 KB of
 //   weight reads to save, the tensor-core kernels run on the adapter-grouped
 //   schedule of group.cuh.
+// The operators around the adapted projection are in layer_ops.cuh.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -74,10 +75,11 @@ constexpr int kMaxDevices = 64;
 
 // Every kernel of this library that holds TMEM allocates at most 256 columns
 // and asks for at least this much dynamic shared memory, so that no more than
-// two of its CTAs fit on one SM (228 KB) and their allocations (2 x 256 of 512
-// columns) never wait for each other, whatever calls run concurrently on
-// other streams: a CTA blocked in tcgen05.alloc while its cluster peers hold
-// TMEM and wait at a cluster barrier could otherwise deadlock.
+// two of its CTAs fit on one SM (228 KB), or all 512 columns and at least twice
+// as much, so that no other such CTA fits beside it.  Their allocations then
+// never wait for each other, whatever calls run concurrently on other streams:
+// a CTA blocked in tcgen05.alloc while its cluster peers hold TMEM and wait at
+// a cluster barrier could otherwise deadlock.
 constexpr size_t kTmemCtaMinSmem = 80 * 1024;
 
 inline bool aligned_to(const void* p, uintptr_t a) {

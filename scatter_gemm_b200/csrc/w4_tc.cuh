@@ -240,6 +240,36 @@ struct W4Tc {
   static_assert(kABufs >= kRing, "a widened block for each set");
 };
 
+// This CTA's share of a tile's outputs from the parts of its cluster's CTAs,
+// [token][row] at `base` of each: four rows of a token a thread at a time, all
+// ranks' loads before the first sum.
+template <class E, bool X8, int NT, int THREADS>
+__device__ __forceinline__ void w4_add_parts(const W4TcParams& P, int tile, int rank,
+                                             uint32_t base, int tid) {
+  const W4Args& p = P.a;
+  const int tb = (tile / P.tiles_n) * NT, n0 = (tile % P.tiles_n) * kW4M;
+  const int c0 = NT * rank / P.cs, c1 = NT * (rank + 1) / P.cs;
+  for (int e = tid; e < (c1 - c0) * (kW4M / 4); e += THREADS) {
+    const int c = c0 + e / (kW4M / 4), r = e % (kW4M / 4) * 4;
+    const int t = tb + c;
+    if (t >= p.tok) break;
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < P.cs) v[i] = ld_dsmem_v4(mapa_shared(base + static_cast<uint32_t>(c * kW4M + r) * 4, i));
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i < P.cs) {
+        v[0].x += v[i].x; v[0].y += v[i].y; v[0].z += v[i].z; v[0].w += v[i].w;
+      }
+    const float f = X8 ? __ldg(p.x_scale + t) : 1.f;
+    const float o[4] = {v[0].x * f, v[0].y * f, v[0].z * f, v[0].w * f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n0 + r + i < p.N) stg16(p.out + t * p.ld_out + n0 + r + i, E::f32_to_bits(o[i]));
+  }
+}
+
 template <class E, bool X8, int NT, int GS, int SETS, int SW>
 __global__ void __launch_bounds__((W4Tc<X8, NT, GS, SETS, SW>::kThreads), 1)
 w4_tc_kernel(const __grid_constant__ W4TcParams P) {
@@ -405,6 +435,15 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
       }
       skip = kb - kb1;
     }
+    // One tile: the parts of the cluster's CTAs are added in rank order, a share
+    // of the tokens by each CTA, by these warps and the scaling ones (in their
+    // own branch: what all roles share would have the fewest registers of all).
+    // A CTA whose waits gave up has recorded it.
+    if (P.cs > 1) {
+      cluster_sync();
+      if (ok) w4_add_parts<E, X8, NT, 32 * C::kTmaWarp>(P, first, rank, sbase, tid);
+      cluster_sync_relaxed();
+    }
   } else if (warp < C::kTmaWarp) {
     // =========================== scaling: sum += scale * accumulator, then the output
     if constexpr (C::kSplit) regs_inc<C::kRegsScale>();
@@ -493,32 +532,8 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
       }
     }
     if (P.cs > 1) {
-      // One tile: the parts of the cluster's CTAs, each CTA adding its share of
-      // the tokens in rank order.  A CTA whose waits gave up has recorded it.
       cluster_sync();
-      const int tb = (first / P.tiles_n) * NT, n0 = (first % P.tiles_n) * kW4M;
-      const int c0 = NT * rank / P.cs, c1 = NT * (rank + 1) / P.cs;
-      for (int e = 32 * w + lane; e < (c1 - c0) * (kW4M / 4); e += 32 * SW) {
-        // four rows of a token; all ranks' loads before the first sum
-        const int c = c0 + e / (kW4M / 4), r = e % (kW4M / 4) * 4;
-        const int t = tb + c;
-        if (t >= p.tok || !ok) continue;
-        float4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < P.cs)
-            v[i] = ld_dsmem_v4(mapa_shared(sbase + static_cast<uint32_t>(c * kW4M + r) * 4, i));
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-          if (i < P.cs) {
-            v[0].x += v[i].x; v[0].y += v[i].y; v[0].z += v[i].z; v[0].w += v[i].w;
-          }
-        const float f = X8 ? __ldg(p.x_scale + t) : 1.f;
-        const float o[4] = {v[0].x * f, v[0].y * f, v[0].z * f, v[0].w * f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + r + i < p.N) stg16(p.out + t * p.ld_out + n0 + r + i, E::f32_to_bits(o[i]));
-      }
+      if (ok) w4_add_parts<E, X8, NT, 32 * C::kTmaWarp>(P, first, rank, sbase, tid);
       cluster_sync_relaxed();
     }
   } else if (warp < C::kMmaWarp) {
@@ -607,8 +622,7 @@ w4_tc_kernel(const __grid_constant__ W4TcParams P) {
   }
   __syncwarp();
 
-  if (P.cs > 1 && (warp < C::kWide || warp >= C::kTmaWarp)) {
-    // the scaling warps' barriers before and after they read the parts
+  if (P.cs > 1 && warp >= C::kTmaWarp) {  // the others' barriers
     cluster_sync();
     cluster_sync_relaxed();
   }

@@ -493,7 +493,7 @@ def test_w4_long_rows_off_the_16_byte_grid():
 def test_w4_paths_and_launches():
     for tok, N, want, launches in ((8, 512, lora.PATH_GENERAL, 1), (9, 19000, lora.PATH_TENSOR, 1),
                                    (9, 512, lora.PATH_TENSOR | lora.PATH_SPLITK, 1),
-                                   # 150 tiles on 148 SMs: a round and two tiles left over
+                                   # 150 tiles on 148 SMs: a wave and two tiles left over
                                    (128, 150 * 128, lora.PATH_TENSOR | lora.PATH_SPLITK, 2)):
         x, sx, q, packed, s, z = w4_inputs(tok, tok, 256, N, "bf16", 128, False, False)
         out = torch.empty(tok, N, dtype=x.dtype, device="cuda")
@@ -505,7 +505,7 @@ def test_w4_paths_and_launches():
 
 @pytest.mark.parametrize("group", [32, 128])
 def test_w4_tiles_left_over(group):
-    # whole rounds of tiles and a few more, rows and tokens ragged
+    # whole waves of tiles and a few more, rows and tokens ragged
     check_w4(6, 130, 640, 75 * 128 + 5, "bf16", group, True)
     check_w4(7, 200, 384, 80 * 128 - 3, "fp16", group, False, x8=True)
 
@@ -654,3 +654,22 @@ def test_a_layer_of_them_in_a_graph(tok):
         assert torch.equal(getattr(s, n), getattr(t, n)), n
     assert torch.equal(s.q8.view(torch.uint8), t.q8.view(torch.uint8))
     assert lora.device_error() == 0
+
+
+def test_w4_tiles_left_over_in_a_graph():
+    # two launches, the second of which starts early, replayed on new inputs
+    x, sx, q, packed, s, z = w4_inputs(50, 140, 512, 76 * 128, "bf16", 64, True, False)
+    x2 = w4_inputs(51, 140, 512, 76 * 128, "bf16", 64, True, False)[0]
+    want = torch.empty(140, 76 * 128, dtype=x.dtype, device="cuda")
+    lora.lora_w4_project(x2, packed, s, want, group_size=64, w_zeros=z)
+    torch.cuda.synchronize()
+    got, after = torch.empty_like(want), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lora.lora_w4_project(x, packed, s, got, group_size=64, w_zeros=z)
+        after.copy_(got)  # what follows sees both launches' tiles
+    for _ in range(3):
+        got.zero_()
+        x.copy_(x2)
+        graph.replay()
+        assert torch.equal(after, want)
