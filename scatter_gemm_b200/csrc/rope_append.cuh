@@ -10,7 +10,9 @@
 // go to slot slots[t] of the caches.  Every value is rounded once, when stored.
 //
 // The bound is the memory traffic: each q/k/v row read once, q and the cache
-// entries written once, and the token's R table entries.
+// entries written once, and the token's R table entries.  8192 tokens of 40 + 8
+// + 8 heads of 128 with three axes: 46 us, 5.2 TB/s (186 us by the general
+// kernel); one token: 2 us.
 #pragma once
 
 #include "common.cuh"
@@ -144,7 +146,9 @@ __device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
 // rotated part; so a pair never leaves its lane and a head's norm is a few
 // shuffles.  A warp takes 32 / LG heads of one token at a time, `steps` times,
 // DEPTH steps' loads under way: with many tokens that reads the token's
-// cosines, sines and slot once for all of its heads.
+// cosines, sines and slot once for all of its heads.  Two steps ahead at 64
+// registers (46 us) beat three and four at 80 (54, 57 us): the warps that fit
+// hide more than the loads that a warp has under way.
 //
 // A block is eight tokens and the same heads of each, so that which slice a
 // head belongs to, and where, is the same arithmetic for all of its threads.
