@@ -379,20 +379,27 @@ LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* resid
  *   w_scales [G, ld_s]     s, of `dtype`, G = ceil(K / group)
  *   w_zeros  [G, ld_s]     z, one byte each, its low four bits read; NULL: 8 everywhere
  *   out      [tok, ld_out] of `dtype`, written (lora_expand then adds the LoRA term).
+ *   workspace, workspace_bytes  optional device scratch, 16-byte aligned (may be NULL / 0), of
+ *                          use only where rows of x are not 16-byte aligned and tok > 16: with
+ *                          lora_w4_workspace_size(tok, K, x_dtype) bytes x is copied to aligned
+ *                          rows first.  Without it W is read again for every 16 tokens, and K is
+ *                          limited by shared memory (about 98,000): LORA_ERR_UNSUPPORTED beyond.
+ *                          Not to be used by another call that runs at the same time.
  * Weights, and e4m3 values of x, are exact in the products; sums are fp32.
  * With up to 8 tokens bf16 values of x of 2^63 and more count as infinite, and
  * products with |x| under 2^-57 lose bits.  A row of x that holds an infinity
  * or a NaN gives values that are not finite, in that row alone.
- * The outputs of a call depend on its sizes and strides and on the GPU, not on
- * what else runs.  out must not overlap the inputs.
- * x rows that are not 16-byte aligned, with more than 8 tokens, re-read W for
- * every 16 tokens, and K is then limited by shared memory (about 98,000):
- * LORA_ERR_UNSUPPORTED beyond, as for sizes from 2^28 (tok: 2^30) on. */
+ * The outputs of a call depend on its sizes, strides and workspace and on the
+ * GPU, not on what else runs.  out must not overlap the inputs.  N or K beyond
+ * 2^28, tok from 2^30 on: LORA_ERR_UNSUPPORTED. */
+LORA_API size_t lora_w4_workspace_size(int tok, int K, lora_dtype x_dtype);
+
 LORA_API lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,
                                      const void* W, int64_t ld_w, const void* w_scales,
                                      const uint8_t* w_zeros, int64_t ld_s, void* out,
                                      int64_t ld_out, int tok, int K, int N, int group,
-                                     lora_dtype x_dtype, lora_dtype dtype, void* stream);
+                                     lora_dtype x_dtype, lora_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* lora_rope_append -- rotates the q and k slices and appends k and v to a paged cache.
  * The q/k/v slices are heads of head_dim columns at the HOST offsets

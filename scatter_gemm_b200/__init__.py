@@ -9,7 +9,8 @@ imported lazily so that the seeded input generators in
 
 __all__ = ["lora_shrink", "lora_expand", "lora_validate", "make_workspace",
            "workspace_size", "LoraError", "lora_rmsnorm", "lora_w4_project",
-           "lora_rope_append", "w4_pack", "w4_unpack", "w4_quantize", "rope_axis_map"]
+           "lora_rope_append", "w4_pack", "w4_unpack", "w4_quantize", "w4_workspace_size",
+           "rope_axis_map"]
 
 
 def __getattr__(name):

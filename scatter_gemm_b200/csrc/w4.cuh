@@ -118,6 +118,34 @@ __device__ __forceinline__ void w4_mma<Fp16>(float (&c)[4], uint32_t a0, uint32_
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Copies rows of `bytes` bytes at any address to 16-byte aligned rows of
+// `pitch` bytes, zeros behind their end: a 16-byte piece a thread, from the two
+// aligned pieces that cover it.
+__global__ void __launch_bounds__(256) align_rows_kernel(const uint8_t* src, const int64_t ld,
+                                                         uint8_t* dst, const int bytes,
+                                                         const int pitch, const int64_t pieces) {
+  const int per = pitch / 16;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  const int64_t t = i / per;
+  const int at = static_cast<int>(i - t * per) * 16;
+  const uint8_t* p = src + t * ld + at;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (at + 16 <= bytes) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4* q = reinterpret_cast<const uint4*>(p - off);
+    v = __ldg(q);
+    if (off) v = bytes_at(v, __ldg(q + 1), off);
+  } else {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (at + e < bytes) w[e / 4] |= static_cast<uint32_t>(__ldg(p + e)) << (8 * (e & 3));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  stg128(dst + i * 16, v);
+}
+
 // What turns packed weights into operands of w4_mv without arithmetic: the bit
 // patterns 0 .. 255 of bf16 and of fp16 are the numbers 0 .. 255 times their
 // smallest subnormal, 2^-133 or 2^-24, so four masked bits are q (or 16 q,

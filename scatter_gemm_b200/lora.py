@@ -82,7 +82,10 @@ def lib() -> ctypes.CDLL:
             l.lora_rmsnorm.argtypes = [_P, _L, _P, _L, _P, _L, _P, _F, _F, _P, _L, _P, _L, _P] + \
                 [_I] * 3 + [_P]
             l.lora_rmsnorm.restype = _I
-            l.lora_w4_project.argtypes = [_P, _L, _P, _P, _L, _P, _P, _L, _P, _L] + [_I] * 6 + [_P]
+            l.lora_w4_project.argtypes = [_P, _L, _P, _P, _L, _P, _P, _L, _P, _L] + [_I] * 6 + \
+                [_P, _Z, _P]
+            l.lora_w4_workspace_size.argtypes = [_I] * 3
+            l.lora_w4_workspace_size.restype = _Z
             l.lora_w4_project.restype = _I
             l.lora_rope_append.argtypes = [_P, _L, _P, _I, _I, _P, _L, _I, _P, _P, _L, _I, _P, _P,
                                            _F, _F, _P, _L, _P, _P, _P, _P, _L, _I, _I, _F, _F, _P,
@@ -455,6 +458,17 @@ def _ld(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> int:
     return _rows(t, name, dtype, shape[0], shape[1], dev)
 
 
+def _scratch(n: int, device: torch.device, stream) -> torch.Tensor:
+    """n bytes that belong to the stream of the call, so that whoever gets them
+    after the call waits for it."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
     """Checks a contiguous 1-D tensor of n elements; returns its address."""
     if t.dtype is not dtype:
@@ -467,7 +481,7 @@ def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> i
 # The words of the packed entry points: q an integer or an address, d a float.
 _WORDS = {
     "lora_rmsnorm": struct.Struct("=7q2d9q").pack,
-    "lora_w4_project": struct.Struct("=17q").pack,
+    "lora_w4_project": struct.Struct("=19q").pack,
     "lora_rope_append": struct.Struct("=17q2d13q2d5q").pack,
 }
 
@@ -541,7 +555,8 @@ def lora_rmsnorm(x: torch.Tensor, weight: torch.Tensor, out: Optional[torch.Tens
 def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tensor,
                     out: torch.Tensor, *, group_size: int,
                     w_zeros: Optional[torch.Tensor] = None,
-                    x_scale: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                    x_scale: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Base projection with 4-bit weights: out = x @ W^T with
     W[n, k] = w_scales[k // group_size, n] * (q[n, k] - w_zeros[k // group_size, n]).
 
@@ -549,7 +564,9 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     with x_scale [tok] (fp32); w_packed [N, >= ceil(K/32)*16] uint8 holds q as
     :func:`w4_pack` lays it out; w_scales [ceil(K/group_size), N] of out's
     type; w_zeros uint8 of the same shape (default: 8 everywhere); out [tok,
-    >= N] is written in its first N columns."""
+    >= N] is written in its first N columns.  A batch of more than 16 tokens
+    whose rows of x are not 16-byte aligned is copied to the workspace first
+    (:func:`w4_workspace_size` bytes; allocated when none is given)."""
     dt = _dtype_code(out)
     x_shape, w_shape = x.shape, w_packed.shape
     if len(x_shape) != 2 or len(w_shape) != 2:
@@ -582,11 +599,26 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     if x_scale is not None:
         ptr_sx = _flat(x_scale, "x_scale", torch.float32, tok, dev)
     ld_o = _ld(out, "out", dtype, (tok, N), dev)
+    ptr_x = x.data_ptr()
+    ws = wsb = 0
+    if tok > 16 and dev >= 0 and (ptr_x | ld_x * x_dtype.itemsize) & 15:
+        if workspace is None:
+            workspace = _scratch(w4_workspace_size(tok, K, x_dtype), x.device, stream)
+        elif workspace.get_device() != dev:
+            raise ValueError("workspace must be on the device of the other tensors")
+        ws, wsb = _ws(workspace)
     if tok and N:
         _call_on(dev, "lora_w4_project",
-                 (x.data_ptr(), ld_x, ptr_sx, w_packed.data_ptr(), ld_w, w_scales.data_ptr(),
-                  ptr_z, ld_s, out.data_ptr(), ld_o, tok, K, N, group_size, x_dt, dt), stream)
+                 (ptr_x, ld_x, ptr_sx, w_packed.data_ptr(), ld_w, w_scales.data_ptr(),
+                  ptr_z, ld_s, out.data_ptr(), ld_o, tok, K, N, group_size, x_dt, dt, ws, wsb),
+                 stream)
     return out
+
+
+def w4_workspace_size(tok: int, K: int, x_dtype: torch.dtype) -> int:
+    """Bytes of workspace that lora_w4_project takes for rows of x that are not
+    16-byte aligned."""
+    return int(lib().lora_w4_workspace_size(tok, K, _CODES[x_dtype]))
 
 
 # the place of value i of eight in a 32-bit word of packed weights

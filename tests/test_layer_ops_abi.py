@@ -45,7 +45,7 @@ def test_norm_argument_checks(L, kw, want):
 
 def w4(lib, **kw):
     a = dict(x=P, ld_x=128, sx=None, W=P, ld_w=64, s=P, z=P, ld_s=16, out=P, ld_out=16, tok=4,
-             K=128, N=16, group=128, xdt=0, dt=0)
+             K=128, N=16, group=128, xdt=0, dt=0, ws=None, wsb=0)
     a.update(kw)
     return lib.lora_w4_project(*a.values(), None)
 
@@ -61,6 +61,7 @@ def w4(lib, **kw):
     (dict(s=None), INVALID), (dict(out=None), INVALID), (dict(x=P + 1), INVALID),
     (dict(s=P + 1), INVALID), (dict(out=P + 1), INVALID),
     (dict(W=P + 8), UNSUPPORTED), (dict(ld_w=72), UNSUPPORTED),
+    (dict(wsb=64), INVALID), (dict(ws=P + 8, wsb=64), INVALID),
     (dict(tok=1 << 30), UNSUPPORTED), (dict(N=(1 << 28) + 1, ld_out=1 << 29, ld_s=1 << 29), UNSUPPORTED),
     (dict(tok=0), OK), (dict(N=0), OK), (dict(tok=0, x=None), OK),
 ])
@@ -220,6 +221,13 @@ def test_w4_quantize(zeros):
         lora.w4_quantize(W.float())
 
 
+def test_w4_workspace_size(L):
+    assert lora.w4_workspace_size(10, 7, torch.bfloat16) == 160
+    assert lora.w4_workspace_size(3, 33, torch.float8_e4m3fn) == 3 * 48
+    assert lora.w4_workspace_size(0, 33, torch.float16) == 0
+    assert L.lora_w4_workspace_size(-1, 3, 0) == 0
+
+
 def test_rope_axis_map():
     assert lora.rope_axis_map([2, 1, 3]) == [0, 0, 1, 2, 2, 2]
     assert lora.rope_axis_map([3, 2, 2], interleaved=True) == [0, 1, 2, 0, 1, 2, 0]
@@ -241,7 +249,7 @@ def test_packed_calls_give_what_the_calls_give(L):
         assert n(**kw) == want, kw
     w = lambda **k: L.lora_w4_project_packed(lora._WORDS["lora_w4_project"](*{**dict(
         x=P, ld_x=128, sx=0, W=P, ld_w=64, s=P, z=P, ld_s=16, out=P, ld_out=16, tok=0, K=128, N=16,
-        group=128, xdt=0, dt=0, st=0), **k}.values()))
+        group=128, xdt=0, dt=0, ws=0, wsb=0, st=0), **k}.values()))
     for kw, want in ((dict(), OK), (dict(xdt=2), INVALID), (dict(group=16), UNSUPPORTED),
                      (dict(ld_out=15), INVALID), (dict(tok=3, W=P + 8), UNSUPPORTED)):
         assert w(**kw) == want, kw

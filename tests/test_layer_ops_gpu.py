@@ -480,6 +480,7 @@ def test_w4_long_rows(tok):
 
 def test_w4_long_rows_off_the_16_byte_grid():
     check_w4(5, 20, 30001, 40, "bf16", 64)
+    # up to 8 tokens nothing is copied, and these rows fit neither kernel
     x = new(2, 120000, torch.bfloat16, pad=1)
     out = new(2, 16, torch.bfloat16)
     with pytest.raises(lora.LoraError) as e:
@@ -673,3 +674,53 @@ def test_w4_tiles_left_over_in_a_graph():
         x.copy_(x2)
         graph.replay()
         assert torch.equal(after, want)
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("given", ["none", "enough", "short"])
+def test_w4_workspace_for_rows_off_the_16_byte_grid(x8, given):
+    # 20 tokens whose rows start at any element: copied to aligned rows first,
+    # or (too short a workspace) read as they are
+    x, sx, q, packed, s, z = w4_inputs(60, 20, 333, 200, "bf16", 64, True, x8, pad=0, lead=3)
+    need = lora.w4_workspace_size(20, 333, x.dtype)
+    ws = None
+    if given != "none":
+        guard = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+        ws = guard[:need if given == "enough" else 16]
+    out = new(20, 200, torch.bfloat16)
+    lora.reset_launch_count()
+    lora.lora_w4_project(x, packed, s, out, group_size=64, w_zeros=z, x_scale=sx, workspace=ws)
+    assert lora.launch_count() == (1 if given == "short" else 2)
+    want = torch.empty_like(out)
+    even = torch.zeros(20, 336, device="cuda").to(x.dtype)[:, :333]
+    if x8:  # rows of 336 bytes are on the grid too
+        assert even.stride(0) % 16 == 0
+    even.copy_(x)
+    lora.lora_w4_project(even, packed, s, want, group_size=64, w_zeros=z, x_scale=sx)
+    if given != "short":
+        assert torch.equal(out, want)
+        if ws is not None:
+            assert (guard[need:] == 0x5A).all()
+    else:
+        # each within half a step of the exact value, and its sums' error
+        tol = want.double().abs() * 2.0 ** -7 + x.double().abs().sum(1)[:, None] * \
+            (1.0 if sx is None else sx.double()[:, None]) * 15 * s.double().max() * 60 * 2.0 ** -21
+        within(out, want.double(), tol, "out")
+
+
+def test_w4_scratch_belongs_to_the_calls_stream():
+    # the scratch of calls on a side stream must not be handed to the current
+    # stream's allocations while those calls run
+    x, sx, q, packed, s, z = w4_inputs(61, 200, 4001, 2048, "bf16", 128, False, False)
+    want = torch.empty(200, 2048, dtype=x.dtype, device="cuda")
+    lora.lora_w4_project(x, packed, s, want, group_size=128)
+    torch.cuda.synchronize()
+    n = lora.w4_workspace_size(200, 4001, x.dtype)
+    for st in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        outs = [torch.empty_like(want) for _ in range(12)]
+        torch.cuda.synchronize()
+        for o in outs:
+            lora.lora_w4_project(x, packed, s, o, group_size=128, stream=st)
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
