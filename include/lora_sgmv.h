@@ -480,7 +480,9 @@ LORA_API lora_status lora_expand_i64(const void* in_r, int64_t ld_in, const void
                                      void* stream);
 
 /* Kernel path (LORA_PATH_* bits) chosen by the last lora_shrink / lora_expand
- * call made on this host thread; 0 if none launched a kernel. */
+ * call made on this host thread; 0 if none launched a kernel.  lora_w4_project
+ * sets LORA_PATH_TENSOR, with LORA_PATH_SPLITK where tiles split K, or
+ * LORA_PATH_GENERAL; lora_rmsnorm and lora_rope_append set LORA_PATH_GENERAL. */
 LORA_API int lora_last_path(void);
 
 /* Failure detection of the tensor-core kernels.  Every mbarrier wait inside

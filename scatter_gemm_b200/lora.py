@@ -486,18 +486,22 @@ _WORDS = {
 }
 
 
+_PACKED = {name: name + "_packed" for name in _WORDS}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _call_on(dev: int, name: str, args, stream, tail: bytes = b"") -> None:
     """Calls a packed entry point with the tensors' device current, on the given
     stream or that device's current one."""
     if dev < 0:
         raise ValueError(f"{name} needs CUDA tensors")
-    fn = getattr(_lib or lib(), name + "_packed")
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        raw = _stream(stream)
-    words = _WORDS[name](*args, raw) + tail
-    if dev == torch._C._cuda_getDevice():
+    fn = getattr(_lib or lib(), _PACKED[name])
+    raw = _raw_stream(dev) if stream is None else _stream(stream)
+    words = _WORDS[name](*args, raw)
+    if tail:
+        words += tail
+    if dev == _current_device():
         st = fn(words)
     else:
         with torch.cuda.device(dev):
@@ -696,18 +700,16 @@ def rope_axis_map(sections: Sequence[int], interleaved: bool = False) -> list:
     return [i % m if i < m * sec[i % m] else 0 for i in range(sum(sec))]
 
 
-def _cache(t: torch.Tensor, name: str, hkv: int, D: int, dev: int):
-    """Checks a [pages, page_size, Hkv, D] cache of any strides but the last;
-    returns the others."""
+def _cache(t: torch.Tensor, name: str, shape, dev: int):
+    """Checks a cache of the given shape and any strides but the last; returns them."""
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the other tensors, got {t.device}")
-    shape = t.shape
-    if len(shape) != 4 or shape[2] != hkv or shape[3] != D:
-        raise ValueError(f"{name} must be [pages, page_size, {hkv}, {D}], got {tuple(shape)}")
-    page, slot, head, inner = t.stride()
-    if inner != 1 and D > 1:
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    strides = t.stride()
+    if strides[3] != 1 and shape[3] > 1:
         raise ValueError(f"{name} must have a unit inner stride")
-    return page, slot, head
+    return strides
 
 
 def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: int,
@@ -775,11 +777,13 @@ def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: 
         elif axes > 1:
             raise ValueError("positions of several axes need an axis_map")
     hkv = (o2 - o1) // D
-    kp, kl, kh = _cache(k_cache, "k_cache", hkv, D, dev)
-    vp, vl, vh = _cache(v_cache, "v_cache", hkv, D, dev)
     c_shape, c_dtype = k_cache.shape, k_cache.dtype
-    if c_shape != v_cache.shape or c_dtype is not v_cache.dtype:
-        raise ValueError("k_cache and v_cache must share shape and element type")
+    if len(c_shape) != 4 or c_shape[2] != hkv or c_shape[3] != D:
+        raise ValueError(f"k_cache must be [pages, page_size, {hkv}, {D}], got {tuple(c_shape)}")
+    kp, kl, kh, _ = _cache(k_cache, "k_cache", c_shape, dev)
+    vp, vl, vh, _ = _cache(v_cache, "v_cache", c_shape, dev)
+    if c_dtype is not v_cache.dtype:
+        raise ValueError("k_cache and v_cache must share their element type")
     c_dt = _CODES.get(c_dtype, -1)
     if c_dt != dt and c_dt != 2:
         raise TypeError(f"the caches must be {dtype} or float8_e4m3fn, got {c_dtype}")
