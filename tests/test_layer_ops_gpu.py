@@ -724,3 +724,41 @@ def test_w4_scratch_belongs_to_the_calls_stream():
             torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for o in outs)
+
+
+def test_norm_offsets_beyond_32_bits():
+    tok, H = 66000, 32776  # over 2^31 elements; the first and last rows count
+    g = gen(70)
+    x = torch.ones(tok, H, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, tok // 2, tok - 2, tok - 1]
+    for r in rows:
+        x[r] = rand(g, H, dtype=x.dtype)
+    w = rand(g, H, dtype=x.dtype)
+    out = torch.zeros_like(x)
+    q = torch.zeros(tok, H, dtype=torch.uint8, device="cuda").view(E4M3)
+    sc = torch.empty(tok, device="cuda")
+    lora.lora_rmsnorm(x, w, out, out_q=q, out_scale=sc)
+    few = torch.empty(len(rows), H, dtype=x.dtype, device="cuda")
+    fq, fs = torch.empty(len(rows), H, dtype=torch.uint8, device="cuda").view(E4M3), torch.empty(len(rows), device="cuda")
+    lora.lora_rmsnorm(x[rows].contiguous(), w, few, out_q=fq, out_scale=fs)
+    # the same thread layout for few rows and many is not given: sums may differ
+    within(out[rows], few.double(), few.double().abs() * 2.0 ** -7, "out")
+    within(sc[rows], fs.double(), fs.double() * 2.0 ** -15, "scale")
+    d = fq.double() * fs.double()[:, None]
+    within(q[rows].double() * sc[rows].double()[:, None], d, d.abs() * 2.0 ** -3 + 2.0 ** -9 * fs.double()[:, None], "q")
+
+
+def test_w4_offsets_beyond_32_bits():
+    tok, K, N = 66000, 64, 32800
+    g = gen(71)
+    x = rand(g, tok, K, dtype=torch.bfloat16)
+    packed = lora.w4_pack(torch.randint(0, 16, (N, K), generator=g, device="cuda"))
+    s = (0.01 * torch.exp(rand(g, 1, N, std=0.3))).to(x.dtype)
+    out = torch.zeros(tok, N, dtype=x.dtype, device="cuda")
+    lora.lora_w4_project(x, packed, s, out, group_size=64)
+    rows = [0, 127, 128, 40000, 65520, tok - 1]
+    xf = torch.zeros(40, K, dtype=x.dtype, device="cuda")
+    xf[:len(rows)] = x[rows]
+    few = torch.empty(40, N, dtype=x.dtype, device="cuda")
+    lora.lora_w4_project(xf, packed, s, few, group_size=64)
+    assert torch.equal(out[rows], few[:len(rows)])  # one group: one sum, however tiled
