@@ -346,7 +346,7 @@ LORA_API lora_status lora_base_expand(const void* x, int64_t ld_x, const void* W
  *   h[t, c] = rn(x[t, c] + residual[t, c])                      (x itself without a residual)
  *   v[t, c] = h[t, c] * rsqrt(sum_c h[t, c]^2 / H + eps) * (weight[c] + weight_offset)
  *   residual_out = h;   out = rn(v);
- *   out_scale[t] = max_c |v[t, c]| / 448;   out_q[t, c] = e4m3(v[t, c] / out_scale[t])
+ *   out_scale[t] = max_c |v[t, c]| / 448;   out_q[t, c] = e4m3(v[t, c] * rn32(1 / out_scale[t]))
  *   x, residual, residual_out, out [tok, ld_*], weight [H]   of `dtype`
  *   out_q [tok, ld_q] e4m3, out_scale [tok] fp32
  * residual and residual_out go together (both NULL: no residual; the same
@@ -355,7 +355,11 @@ LORA_API lora_status lora_base_expand(const void* x, int64_t ld_x, const void* W
  * residual, row on row; other overlaps are undefined.  The row's sum, its
  * factor and v are fp32.  A row of zeros (or one whose scale would be below
  * the smallest normal fp32) has scale 0 and zeros.  A row with an infinity or
- * a NaN has a NaN scale.
+ * a NaN has a NaN scale.  The sum of squares is an fp32 value: a row where it
+ * passes fp32's range (a root mean square above 2^64 / sqrt(H)) has the factor 0.
+ * The product with the reciprocal, itself rounded to fp32 (rn32), is within 2^-23 of
+ * the quotient; where that lies on the border between two e4m3 values, the
+ * division and the product may take different ones.
  * H > LORA_MAX_NORM_WIDTH: LORA_ERR_UNSUPPORTED. */
 #define LORA_MAX_NORM_WIDTH 65536
 LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* residual,
@@ -415,9 +419,10 @@ LORA_API lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x
  * The results are rounded once:
  *   q_out    [tok, ld_q]         of `dtype`; may be the q slice of qkv itself
  *   k_cache, v_cache             head h of slot s at page*strides[0] + (s % page_size)*strides[1]
- *                                + h*strides[2], page = s / page_size: rn(k' / k_scale) and
- *                                rn(v / v_scale); strides (HOST, elements) of each cache;
- *                                cache_dtype is `dtype` or LORA_E4M3
+ *                                + h*strides[2], page = s / page_size: rn(k' * rn32(1 / k_scale))
+ *                                and rn(v * rn32(1 / v_scale)), as for out_q above; strides
+ *                                (HOST, elements) of each cache; cache_dtype is `dtype` or
+ *                                LORA_E4M3
  *   slots    [tok]               the cache slot of each token; a token whose slot is negative
  *                                or at least num_pages*page_size writes no cache entry.
  *                                Slots of one call must differ: of equal ones any token's

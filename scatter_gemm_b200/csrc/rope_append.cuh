@@ -6,7 +6,7 @@
 //   a' = a cos[p, i] - b sin[p, i],   b' = b cos[p, i] + a sin[p, i]
 // in fp32; elements behind the first R pass through.  With head weights each
 // head of q and k is first normalised: x * rsqrt(mean x^2 + eps) * (w + w0).
-// q goes to q_out; k' and v, divided by their cache's scale for an 8-bit cache,
+// q goes to q_out; k' and v, times the fp32 reciprocal of their cache's scale,
 // go to slot slots[t] of the caches.  Every value is rounded once, when stored.
 //
 // The bound is the memory traffic: each q/k/v row read once, q and the cache

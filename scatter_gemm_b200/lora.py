@@ -729,8 +729,8 @@ def lora_rope_append(qkv: torch.Tensor, slice_offsets: Sequence[int], head_dim: 
     [axes, tok] with axis_map (one axis number for each frequency, see
     :func:`rope_axis_map`); cos_sin [max_pos, R] fp32, R/2 cosines and R/2
     sines, R <= head_dim even; k_cache, v_cache [pages, page_size, Hkv,
-    head_dim] of qkv's type or float8_e4m3fn (values divided by k_scale,
-    v_scale), any strides but a unit inner one; slots [tok], negative = no
+    head_dim] of qkv's type or float8_e4m3fn (values times the fp32
+    reciprocal of k_scale, v_scale), any strides but a unit inner one; slots [tok], negative = no
     cache entry.  positions and slots are both int32 or both int64.  q_weight
     and k_weight [head_dim] normalise each head first.  q_out [tok, Hq *
     head_dim] defaults to the q slice itself, in place."""
