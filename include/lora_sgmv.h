@@ -389,10 +389,9 @@ LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* resid
  *                          rows first.  Without it W is read again for every 16 tokens, and K is
  *                          limited by shared memory (about 98,000): LORA_ERR_UNSUPPORTED beyond.
  *                          Not to be used by another call that runs at the same time.
- * Weights, and e4m3 values of x, are exact in the products; sums are fp32.
- * With up to 8 tokens bf16 values of x of 2^63 and more count as infinite, and
- * products with |x| under 2^-57 lose bits.  A row of x that holds an infinity
- * or a NaN gives values that are not finite, in that row alone.
+ * q - z, and e4m3 values of x, are exact in the products; sums are fp32.  An
+ * infinity in x adds its product with q - z: an infinity, or a NaN where q = z.
+ * A row of x that holds an infinity or a NaN does not change other rows.
  * The outputs of a call depend on its sizes, strides and workspace and on the
  * GPU, not on what else runs.  out must not overlap the inputs.  N or K beyond
  * 2^28, tok from 2^30 on: LORA_ERR_UNSUPPORTED. */

@@ -295,20 +295,19 @@ bool encode_w4(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint6
 constexpr int kW4Smem = 227 * 1024;
 constexpr int kMvSmem = 200 * 1024;
 
-// Shared memory of w4_mv for tt tokens: staged x and its sums, and two tiles' parts.
-template <int NT, int VW>
+// Shared memory of w4_mv for tt tokens: staged x, and two tiles' parts.
+template <int NT>
 int64_t w4_mv_bytes(int64_t tt, int K) {
   const int64_t blocks = (K + 127) / 128;
-  return tt * lora::mv_row_bytes(static_cast<int>(blocks) * 128) + blocks * (4 / VW) * NT * 32 +
-         2 * lora::kMvWarps * NT * 512;
+  return tt * lora::mv_row_bytes(static_cast<int>(blocks) * 128) + 2 * lora::kMvWarps * NT * 512;
 }
 
 template <class E, bool X8, int NT, int VW>
 lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
   const int tiles = (a.N + 15) / 16;
   int tt = std::min(a.tok, 8 * NT);
-  while (tt > 1 && w4_mv_bytes<NT, VW>(tt, a.K) > kMvSmem) --tt;
-  const int64_t bytes = w4_mv_bytes<NT, VW>(tt, a.K);
+  while (tt > 1 && w4_mv_bytes<NT>(tt, a.K) > kMvSmem) --tt;
+  const int64_t bytes = w4_mv_bytes<NT>(tt, a.K);
   if (bytes > kMvSmem || a.ld_s >= (int64_t(1) << 31)) return LORA_ERR_UNSUPPORTED;
   const int smem = static_cast<int>(bytes);
   const int64_t gy = (a.tok + tt - 1) / tt;
@@ -459,7 +458,7 @@ lora_status w4_project_group(lora::W4Args a, void* ws, size_t ws_bytes, int sms,
   // 24576: 21 us, against 28 with w4_tc; 9 at 4096 x 6144: 12.6 against 11.5),
   // so beyond that it only takes what TMA cannot; it needs all of K's x in
   // shared memory.
-  const bool fits = w4_mv_bytes<1, VW>(std::min(a.tok, 8), a.K) <= kMvSmem;
+  const bool fits = w4_mv_bytes<1>(std::min(a.tok, 8), a.K) <= kMvSmem;
   if ((a.tok <= 8 && fits) || !tma_x)
     return a.tok <= 8 ? w4_mv<E, X8, 1, VW>(a, sms, st) : w4_mv<E, X8, 2, VW>(a, sms, st);
   if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4, 4>(a, sms, st);

@@ -5,10 +5,10 @@
 //
 // Eight weights are one 32-bit word, value i of the word at bit
 // (0, 16, 4, 20, 8, 24, 12, 28)[i]: one mask after shifts by 0, 4, 8 and 12
-// gives the pairs (0, 1), (2, 3), (4, 5), (6, 7) in the halves of a register,
-// next to the exponent bits that make them 128 + q (bf16) or 1024 + q (fp16).
-// Subtracting 128 + z or 1024 + z is exact, so the products of a group are
-// exact too; a group's sum is scaled in fp32 before it joins the others.
+// gives the pairs (0, 1), (2, 3), (4, 5), (6, 7) in the halves of a register.
+// What is multiplied is q - z, which is exact in either element type, so the
+// products of a group are exact too and a weight at its zero point adds nothing
+// whatever its x; a group's sum is scaled in fp32 before it joins the others.
 #pragma once
 
 #include <type_traits>
@@ -33,7 +33,8 @@ struct W4Args {
   int tok, K, N, group_shift;
 };
 
-// The bits that turn the low four bits of each half into a number, and that number.
+// w4_tc's way from q to q - z: exponent bits next to the low four bits of each
+// half make 128 + q (bf16) or 1024 + q (fp16), and 128 + z or 1024 + z is taken off.
 template <class E> struct W4Magic;
 template <> struct W4Magic<Bf16> {
   static constexpr uint32_t kBits = 0x43004300u;  // 128 + q
@@ -146,18 +147,41 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const uint8_t* src, con
   stg128(dst + i * 16, v);
 }
 
-// What turns packed weights into operands of w4_mv without arithmetic: the bit
-// patterns 0 .. 255 of bf16 and of fp16 are the numbers 0 .. 255 times their
-// smallest subnormal, 2^-133 or 2^-24, so four masked bits are q (or 16 q,
-// where they stand four places up) as they are.  bf16 products are kept in
-// fp32's normal range by taking x times 2^64: values of x from 2^63 on become
-// infinite, and products of |x| under 2^-57 lose bits.
-template <class E> struct MvScale;
-template <> struct MvScale<Bf16> {
-  static constexpr float kX = 0x1p64f, kOut = 0x1p69f;
+// w4_mv's way, with half the shifts: a row's zero point z, and what turns its
+// packed weights into (q - z) / kOut, exactly.  The bit patterns 0 .. 255 of bf16
+// and of fp16 are the numbers 0 .. 255 times their smallest subnormal, 2^-133 or
+// 2^-24, so four masked bits are q times that, or 16 q where they stand four
+// places up: one mask and one fused multiply-add a pair.  (By w4_pairs 24.3
+// against 19.3 us for one token, 26.2 against 21.3 us for eight at 4096 x 24576.
+// Products of the bare patterns, with z times the group's sum of x taken off
+// behind them, took as long as this, lost x outside 2^-57 .. 2^64 in bf16 and
+// gave the sums the error of x q rather than of x (q - z).)
+template <class E> struct MvZero;
+template <> struct MvZero<Bf16> {
+  static constexpr float kOut = 0x1p6f;
+  __nv_bfloat162 z;
+  __device__ __forceinline__ explicit MvZero(uint32_t zero)
+      : z(__float2bfloat162_rn(static_cast<float>(zero & 15) * (-1.f / kOut))) {}
+  template <int SHIFT>
+  __device__ __forceinline__ uint32_t pair(uint32_t w) const {
+    w &= 0x000F000Fu << SHIFT;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w),
+                                     __float2bfloat162_rn(0x1p127f / (1 << SHIFT)), z);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
 };
-template <> struct MvScale<Fp16> {
-  static constexpr float kX = 1.f, kOut = 0x1p24f;
+template <> struct MvZero<Fp16> {
+  static constexpr float kOut = 0x1p9f;
+  __half2 z;
+  __device__ __forceinline__ explicit MvZero(uint32_t zero)
+      : z(__float2half2_rn(static_cast<float>(zero & 15) * (-1.f / kOut))) {}
+  template <int SHIFT>
+  __device__ __forceinline__ uint32_t pair(uint32_t w) const {
+    w &= 0x000F000Fu << SHIFT;
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&w),
+                              __float2half2_rn(0x1p15f / (1 << SHIFT)), z);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
 };
 
 constexpr int kMvDepth = 4;  // blocks of 128 K that a warp has in flight
@@ -180,11 +204,8 @@ struct MvBlock {
 // and goes over tiles of 16 weight rows; its warps share the K range, each
 // reading weights straight into registers, several blocks ahead, and multiply
 // by mma.sync (16 rows x 8 tokens x 16 K): one fragment of weights serves
-// eight tokens without a trip through shared memory.  The weights enter as the
-// unsigned q; with xs, the sum of the group's x,
-//   sum_k x (q - z) = sum_k x q - z xs
-// at the cost of one bit of the fp32 sums, and widening a word takes one shift
-// and four masks.
+// eight tokens without a trip through shared memory.  Widening a word takes one
+// shift, four masks and four fused multiply-adds.
 //
 // The pairs of a fragment may be any 16 values of k as long as both operands
 // agree.  Lane t of a row takes VW neighbouring words, so that one load is
@@ -213,14 +234,15 @@ w4_mv_kernel(const W4Args p, const int tt) {
   constexpr int kSub = 4 / VW;  // groups of a block
   constexpr int WARPS = kMvWarps, kThreads = kMvThreads;
   constexpr int kPart = NT * 128;  // sums of a tile
+  // two chains of products a group where there is one fragment of tokens
+  constexpr bool kTwo = NT == 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int t0 = blockIdx.y * tt;
   const int ntok = min(tt, p.tok - t0);
   const int blocks = (p.K + 127) / 128;
   const int rowb = mv_row_bytes(blocks * 128);
-  float* xs = reinterpret_cast<float*>(mv_smem + tt * rowb);  // [groups][8 NT]: sums of x / kOut
-  float* part = xs + blocks * kSub * 8 * NT;                  // [2][WARPS][8 NT][16]
+  float* part = reinterpret_cast<float*>(mv_smem + tt * rowb);  // [2][WARPS][8 NT][16]
   const int tiles = (p.N + 15) / 16;
   const int run0 = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.x / gridDim.x);
   const int run1 = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -363,20 +385,8 @@ w4_mv_kernel(const W4Args p, const int tt) {
                             << (16 * (e & 1));
           }
         }
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = C::u32_to_f2(o[e]);
-          sum += f.x + f.y;
-          if (MvScale<C>::kX != 1.f)
-            o[e] = C::f2_to_u32(f.x * MvScale<C>::kX, f.y * MvScale<C>::kX);
-        }
-        // the 4*VW lanes of a group add their chunks
-#pragma unroll
-        for (int d = 2 * VW; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (live) {
           const int in = cc[i] & (4 * VW - 1);
-          if (in == 0) xs[cc[i] / (4 * VW) * (8 * NT) + rr[i]] = sum * (1.f / MvScale<C>::kOut);
           const int at = (cc[i] - in) + (in % VW) * 4 + in / VW;
           // a product takes pairs 0 and 2 or 1 and 3 of a word: neighbours here
           *reinterpret_cast<uint4*>(mv_smem + rr[i] * rowb + at * 16) =
@@ -419,7 +429,7 @@ w4_mv_kernel(const W4Args p, const int tt) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) v += rb[w * kPart + e];
-        v *= MvScale<C>::kOut;
+        v *= MvZero<C>::kOut;
         if (X8) v *= __ldg(p.x_scale + t0 + tk);
         stg16(p.out + (t0 + tk) * p.ld_out + row, E::f32_to_bits(v));
       }
@@ -446,32 +456,37 @@ w4_mv_kernel(const W4Args p, const int tt) {
           sz0 = __shfl_sync(0xffffffffu, sz0, (lane & ~3) + sub);
           sz1 = __shfl_sync(0xffffffffu, sz1, (lane & ~3) + sub);
         }
-        float g1[NT][4], g2[NT][4];
+        const MvZero<C> z0(sz0 >> 16), z1(sz1 >> 16);
+        float g1[NT][4], g2[kTwo ? NT : 1][4];
 #pragma unroll
         for (int j = 0; j < VW; ++j) {
-          constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;  // q, 16 q
           const uint32_t a = b.w[0][sub * VW + j], e = b.w[1][sub * VW + j];
           const uint32_t a8 = a >> 8, e8 = e >> 8;
+          const uint32_t p0 = z0.template pair<0>(a), p1 = z0.template pair<4>(a),
+                         p2 = z0.template pair<0>(a8), p3 = z0.template pair<4>(a8);
+          const uint32_t q0 = z1.template pair<0>(e), q1 = z1.template pair<4>(e),
+                         q2 = z1.template pair<0>(e8), q3 = z1.template pair<4>(e8);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint4 xv =
                 *reinterpret_cast<const uint4*>(xr[n] + blk * 256 + (sub * VW + j) * 64);
-            w4_mma<C>(g1[n], a & kLo, e & kLo, a8 & kLo, e8 & kLo, xv.x, xv.y, j == 0);
-            w4_mma<C>(g2[n], a & kHi, e & kHi, a8 & kHi, e8 & kHi, xv.z, xv.w, j == 0);
+            w4_mma<C>(g1[n], p0, q0, p2, q2, xv.x, xv.y, j == 0);
+            if constexpr (kTwo)
+              w4_mma<C>(g2[n], p1, q1, p3, q3, xv.z, xv.w, j == 0);
+            else
+              w4_mma<C>(g1[n], p1, q1, p3, q3, xv.z, xv.w, false);
           }
         }
         const float s0 = E::bits_to_f32(static_cast<uint16_t>(sz0));
         const float s1 = E::bits_to_f32(static_cast<uint16_t>(sz1));
-        const float z0 = -static_cast<float>((sz0 >> 16) & 15);
-        const float z1 = -static_cast<float>((sz1 >> 16) & 15);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float2 x2 = *reinterpret_cast<const float2*>(xs + (blk * kSub + sub) * (8 * NT) +
-                                                             8 * n + 2 * t4);
-          acc[n][0] = fmaf(s0, fmaf(z0, x2.x, fmaf(g2[n][0], 0.0625f, g1[n][0])), acc[n][0]);
-          acc[n][1] = fmaf(s0, fmaf(z0, x2.y, fmaf(g2[n][1], 0.0625f, g1[n][1])), acc[n][1]);
-          acc[n][2] = fmaf(s1, fmaf(z1, x2.x, fmaf(g2[n][2], 0.0625f, g1[n][2])), acc[n][2]);
-          acc[n][3] = fmaf(s1, fmaf(z1, x2.y, fmaf(g2[n][3], 0.0625f, g1[n][3])), acc[n][3]);
+          if constexpr (kTwo) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g1[n][i] += g2[n][i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(i < 2 ? s0 : s1, g1[n][i], acc[n][i]);
         }
       }
       fetch(buf[d]);

@@ -49,3 +49,76 @@ def test_rope_cache_values_are_products_with_the_rounded_reciprocal(tok, D, c8):
         assert torch.equal(c.float().reshape(tok, -1), want.float())
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("tok,lead", [(1, 0), (5, 0), (8, 0), (9, 0), (13, 1), (40, 0)])
+def test_w4_range_of_bf16_x(tok, lead, zeros):
+    # rows of x from near the smallest to near the largest normal bf16, one of
+    # both: a row's result does not depend on how many others there are
+    _, _, q, packed, s, z = w4_inputs(91, tok, 520, 70, "bf16", 64, zeros, False)
+    g = gen(92)
+    x = rand(g, tok, 520)
+    mags = [1e-33, 1e35, 1e-20, 1e20, 1.0]
+    for t in range(tok):
+        x[t] *= mags[(t + tok) % 5]
+    x[0, ::2] *= 1e-25 if mags[tok % 5] > 1e-6 else 1e25
+    x = strided(x.bfloat16(), 0, lead)
+    out = new(tok, 70, x.dtype)
+    lora.lora_w4_project(x, packed, s, out, group_size=64, w_zeros=z)
+    of = torch.arange(520, device="cuda") // 64
+    W = (q.double() - (8.0 if z is None else z.double()[of].T)) * s.double()[of].T
+    ref, mag = x.double() @ W.T, x.double().abs() @ W.abs().T
+    depth = 64 / 16 + 9 + 40
+    # TINY: results near the smallest normal value are rounded among subnormals
+    within(out, ref, ref.abs() * 2.0 ** -8 + mag * depth * 2.0 ** -22 + 2.0 ** -133, "out")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("tok,lead", [(1, 0), (6, 0), (9, 0), (14, 3), (30, 0), (100, 0)])
+def test_w4_infinities_are_products_of_their_weights(tok, lead, group, dtype):
+    # inf * (q - z): an infinity of the weight's sign, NaN where q = z
+    x, _, q, packed, s, z = w4_inputs(93, tok, 300, 90, dtype, group, True, False, lead=lead)
+    rows = [0] if tok == 1 else [1, tok - 1]
+    x[rows[0], 77] = float("inf")
+    x[rows[-1], 299] = float("-inf")
+    out = new(tok, 90, x.dtype)
+    lora.lora_w4_project(x, packed, s, out, group_size=group, w_zeros=z)
+    of = torch.arange(300, device="cuda") // group
+    d = q.double() - z.double()[of].T
+    W = d * s.double()[of].T
+    assert (d[:, 77] == 0).any() and (d[:, 77] > 0).any() and (d[:, 77] < 0).any()
+    hit = torch.zeros(tok, dtype=torch.bool, device="cuda")
+    hit[rows] = True
+    want = x.double() @ W.T
+    assert torch.equal(out[hit].double().nan_to_num(7.0), want[hit].nan_to_num(7.0))
+    rest, mag = want[~hit], x[~hit].double().abs() @ W.abs().T
+    within(out[~hit], rest, rest.abs() * HALF[x.dtype] + mag * 60 * 2.0 ** -22 + TINY[x.dtype], "rest")
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("tok,lead", [(1, 0), (8, 0), (12, 1), (20, 0)])
+def test_w4_weights_at_their_zero_point_add_nothing(tok, lead, x8):
+    # columns of large x whose weights all equal their zero point, as in a
+    # pruned model: what is left is a sum of small products
+    _, _, q, _, s, z = w4_inputs(94, tok, 256, 100, "fp16", 64, True, x8)
+    of = torch.arange(256, device="cuda") // 64
+    big = torch.tensor([5, 70, 77, 130, 255], device="cuda")
+    q[:, big] = z.long()[of[big]].T
+    g = gen(95)
+    x = rand(g, tok, 256, std=0.01)
+    x[:, big] = rand(g, tok, 5, std=200.0)
+    sx = None
+    if x8:
+        sx = torch.full((tok,), 2.0, device="cuda")
+        x = (x / 2).clamp(-448, 448).to(E4M3)
+    else:
+        x = x.half()
+    x = strided(x, 0, lead)
+    out = new(tok, 100, torch.float16)
+    lora.lora_w4_project(x, lora.w4_pack(q), s, out, group_size=64, w_zeros=z, x_scale=sx)
+    W = (q.double() - z.double()[of].T) * s.double()[of].T
+    f = 1.0 if sx is None else sx.double()[:, None]
+    ref, mag = (x.double() @ W.T) * f, (x.double().abs() @ W.abs().T) * f
+    within(out, ref, ref.abs() * 2.0 ** -11 + mag * 60 * 2.0 ** -22 + 2.0 ** -25, "out")
+
+
