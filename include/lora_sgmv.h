@@ -384,10 +384,14 @@ LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* resid
  *   w_zeros  [G, ld_s]     z, one byte each, its low four bits read; NULL: 8 everywhere
  *   out      [tok, ld_out] of `dtype`, written (lora_expand then adds the LoRA term).
  *   workspace, workspace_bytes  optional device scratch, 16-byte aligned (may be NULL / 0), of
- *                          use only where rows of x are not 16-byte aligned and tok > 16: with
- *                          lora_w4_workspace_size(tok, K, x_dtype) bytes x is copied to aligned
- *                          rows first.  Without it W is read again for every 16 tokens, and K is
- *                          limited by shared memory (about 98,000): LORA_ERR_UNSUPPORTED beyond.
+ *                          use only where rows of x are not 16-byte aligned and
+ *                          lora_w4_copies_x(tok, K) is 1: more than 16 tokens, or more than
+ *                          shared memory holds (one to K = 94,080, 8 to 11,648, 16 to 5,248).
+ *                          With lora_w4_workspace_size(tok, K, x_dtype) bytes x is then copied
+ *                          to aligned rows first.  Without them W is read again for each lot of
+ *                          tokens that shared memory holds, 16 at most; where it does not hold
+ *                          one (K over 94,080, or 85,888 with more than 8 tokens), or with more
+ *                          than 65,535 lots: LORA_ERR_UNSUPPORTED.
  *                          Not to be used by another call that runs at the same time.
  * q - z, and e4m3 values of x, are exact in the products; sums are fp32.  An
  * infinity in x adds its product with q - z: an infinity, or a NaN where q = z.
@@ -396,6 +400,7 @@ LORA_API lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* resid
  * GPU, not on what else runs.  out must not overlap the inputs.  N or K beyond
  * 2^28, tok from 2^30 on: LORA_ERR_UNSUPPORTED. */
 LORA_API size_t lora_w4_workspace_size(int tok, int K, lora_dtype x_dtype);
+LORA_API int lora_w4_copies_x(int tok, int K);
 
 LORA_API lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,
                                      const void* W, int64_t ld_w, const void* w_scales,

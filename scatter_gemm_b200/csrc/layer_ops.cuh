@@ -302,6 +302,17 @@ int64_t w4_mv_bytes(int64_t tt, int K) {
   return tt * lora::mv_row_bytes(static_cast<int>(blocks) * 128) + 2 * lora::kMvWarps * NT * 512;
 }
 
+// Whether w4_mv holds the rows of x of up to 16 tokens at once.
+inline bool w4_mv_holds(int tok, int K) {
+  return (tok <= 8 ? w4_mv_bytes<1>(tok, K) : w4_mv_bytes<2>(std::min(tok, 16), K)) <= kMvSmem;
+}
+
+// Whether rows of x that TMA cannot load are copied to rows that it can (where
+// there is a workspace): from 17 tokens on, and where w4_mv would read the
+// weights more than once (13 x 8191 x 6144, twice: 37.9 us, copied 21.5).  Where
+// it reads them once it is the faster (13 x 3583 x 6159: 16.5, copied 18.2).
+inline bool w4_copies(int tok, int K) { return tok > 16 || !w4_mv_holds(tok, K); }
+
 template <class E, bool X8, int NT, int VW>
 lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
   const int tiles = (a.N + 15) / 16;
@@ -441,9 +452,7 @@ lora_status w4_project_group(lora::W4Args a, void* ws, size_t ws_bytes, int sms,
   const int64_t ldb = a.ld_x * (X8 ? 1 : 2);
   bool tma_x = aligned_to(a.x, 16) && ldb % 16 == 0;
   const int64_t pitch = w4_pitch(a.K, X8);
-  if (!tma_x && a.tok > 16 && ws && ws_bytes >= static_cast<size_t>(a.tok * pitch)) {
-    // Rows that TMA can load; up to 16 tokens w4_mv as they are is faster (13 x
-    // 3583 x 6159: 15.7 against 18.2 us).
+  if (!tma_x && w4_copies(a.tok, a.K) && ws && ws_bytes >= static_cast<size_t>(a.tok * pitch)) {
     const int64_t pieces = a.tok * (pitch / 16);
     lora::align_rows_kernel<<<static_cast<unsigned>((pieces + 255) / 256), 256, 0, st>>>(
         static_cast<const uint8_t*>(a.x), ldb, static_cast<uint8_t*>(ws), a.K * (X8 ? 1 : 2),
@@ -455,11 +464,10 @@ lora_status w4_project_group(lora::W4Args a, void* ws, size_t ws_bytes, int sms,
     tma_x = true;
   }
   // w4_mv reads the weights once for eight tokens at a time (8 tokens at 4096 x
-  // 24576: 21 us, against 28 with w4_tc; 9 at 4096 x 6144: 12.6 against 11.5),
+  // 24576: 21 us, against 28 with w4_tc; 9 at 4096 x 6144: 12.6 against 10.7),
   // so beyond that it only takes what TMA cannot; it needs all of K's x in
   // shared memory.
-  const bool fits = w4_mv_bytes<1>(std::min(a.tok, 8), a.K) <= kMvSmem;
-  if ((a.tok <= 8 && fits) || !tma_x)
+  if ((a.tok <= 8 && w4_mv_holds(a.tok, a.K)) || !tma_x)
     return a.tok <= 8 ? w4_mv<E, X8, 1, VW>(a, sms, st) : w4_mv<E, X8, 2, VW>(a, sms, st);
   if (a.tok <= 16) return w4_tc<E, X8, 16, GS, 4, 4>(a, sms, st);
   if (a.tok <= 32) return w4_tc<E, X8, 32, GS, 4, 4>(a, sms, st);
@@ -480,6 +488,10 @@ lora_status w4_project(const lora::W4Args& a, void* ws, size_t ws_bytes, int sms
 extern "C" size_t lora_w4_workspace_size(int tok, int K, lora_dtype x_dtype) {
   if (tok < 0 || K < 0) return 0;
   return static_cast<size_t>(tok * w4_pitch(K, x_dtype == LORA_E4M3));
+}
+
+extern "C" int lora_w4_copies_x(int tok, int K) {
+  return tok > 0 && K > 0 && K <= (1 << 28) && w4_copies(tok, K);
 }
 
 extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x_scale,

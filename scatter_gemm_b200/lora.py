@@ -86,6 +86,8 @@ def lib() -> ctypes.CDLL:
                 [_P, _Z, _P]
             l.lora_w4_workspace_size.argtypes = [_I] * 3
             l.lora_w4_workspace_size.restype = _Z
+            l.lora_w4_copies_x.argtypes = [_I] * 2
+            l.lora_w4_copies_x.restype = _I
             l.lora_w4_project.restype = _I
             l.lora_rope_append.argtypes = [_P, _L, _P, _I, _I, _P, _L, _I, _P, _P, _L, _I, _P, _P,
                                            _F, _F, _P, _L, _P, _P, _P, _P, _L, _I, _I, _F, _F, _P,
@@ -568,9 +570,11 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     with x_scale [tok] (fp32); w_packed [N, >= ceil(K/32)*16] uint8 holds q as
     :func:`w4_pack` lays it out; w_scales [ceil(K/group_size), N] of out's
     type; w_zeros uint8 of the same shape (default: 8 everywhere); out [tok,
-    >= N] is written in its first N columns.  A batch of more than 16 tokens
-    whose rows of x are not 16-byte aligned is copied to the workspace first
-    (:func:`w4_workspace_size` bytes; allocated when none is given)."""
+    >= N] is written in its first N columns.  Rows of x that are not 16-byte
+    aligned are copied to the workspace first (:func:`w4_workspace_size` bytes)
+    where there are more than 16 of them, or more than shared memory holds.  It
+    is allocated when none is given, unless up to 16 rows are so long (K over
+    94,080) that shared memory does not hold one: those need a given one."""
     dt = _dtype_code(out)
     x_shape, w_shape = x.shape, w_packed.shape
     if len(x_shape) != 2 or len(w_shape) != 2:
@@ -605,12 +609,15 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     ld_o = _ld(out, "out", dtype, (tok, N), dev)
     ptr_x = x.data_ptr()
     ws = wsb = 0
-    if tok > 16 and dev >= 0 and (ptr_x | ld_x * x_dtype.itemsize) & 15:
-        if workspace is None:
+    if dev >= 0 and (ptr_x | ld_x * x_dtype.itemsize) & 15 and \
+            (tok > 16 or lib().lora_w4_copies_x(tok, K)):
+        if workspace is not None:
+            if workspace.get_device() != dev:
+                raise ValueError("workspace must be on the device of the other tensors")
+        elif tok > 16 or not lib().lora_w4_copies_x(1, K):
             workspace = _scratch(w4_workspace_size(tok, K, x_dtype), x.device, stream)
-        elif workspace.get_device() != dev:
-            raise ValueError("workspace must be on the device of the other tensors")
-        ws, wsb = _ws(workspace)
+        if workspace is not None:
+            ws, wsb = _ws(workspace)
     if tok and N:
         _call_on(dev, "lora_w4_project",
                  (ptr_x, ld_x, ptr_sx, w_packed.data_ptr(), ld_w, w_scales.data_ptr(),

@@ -122,3 +122,49 @@ def test_w4_weights_at_their_zero_point_add_nothing(tok, lead, x8):
     within(out, ref, ref.abs() * 2.0 ** -11 + mag * 60 * 2.0 ** -22 + 2.0 ** -25, "out")
 
 
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("K", [8191, 16383, 70001])
+@pytest.mark.parametrize("tok", [6, 8, 9, 16])
+def test_w4_long_rows_off_the_grid_are_copied(tok, K, x8):
+    # where shared memory does not hold all tokens' rows at once, the rows are
+    # copied to the workspace and W is read once
+    check_w4(tok, tok, K, 40, "bf16", 128, False, x8)
+    copies = lora.lib().lora_w4_copies_x(tok, K)
+    assert bool(lora.last_path() & lora.PATH_TENSOR) == bool(copies)
+    assert copies == ((tok, K) not in ((6, 8191), (8, 8191), (9, 8191)))
+
+
+@pytest.mark.parametrize("tok,most", [(1, 94080), (3, 94080), (9, 85888), (40, 85888)])
+def test_w4_long_rows_off_the_grid_without_a_workspace(tok, most):
+    # as long as shared memory holds one of them
+    for K, want in ((most, lora.LORA_OK), (most + 1, lora.LORA_ERR_UNSUPPORTED)):
+        x, _, q, packed, s, z = w4_inputs(tok, tok, K, 20, "bf16", 128, False, False, lead=1)
+        out = new(tok, 20, x.dtype)
+        got = lora.lib().lora_w4_project(
+            x.data_ptr(), x.stride(0), None, packed.data_ptr(), packed.stride(0), s.data_ptr(), None,
+            s.stride(0), out.data_ptr(), out.stride(0), tok, K, 20, 128, 0, 0, None, 0,
+            torch.cuda.current_stream().cuda_stream)
+        assert got == want
+        if want:
+            assert (out == SENT).all()
+            continue
+        W = (q.double() - 8) * s.double()[torch.arange(K, device="cuda") // 128].T
+        ref, mag = x.double() @ W.T, x.double().abs() @ W.abs().T
+        depth = 128 / 16 + -(-K // 128) + 40
+        within(out, ref, ref.abs() * 2.0 ** -8 + mag * depth * 2.0 ** -22, "out")
+
+
+@pytest.mark.parametrize("tok", [1, 2, 16])
+def test_w4_longest_rows_off_the_grid_take_a_given_workspace(tok):
+    K = 120000
+    x, _, q, packed, s, z = w4_inputs(5, tok, K, 20, "fp16", 128, False, False, lead=1)
+    out, want = new(tok, 20, x.dtype), new(tok, 20, x.dtype)
+    with pytest.raises(lora.LoraError):
+        lora.lora_w4_project(x, packed, s, out, group_size=128)
+    assert (out == SENT).all()
+    ws = torch.empty(lora.w4_workspace_size(tok, K, x.dtype), dtype=torch.uint8, device="cuda")
+    lora.lora_w4_project(x, packed, s, out, group_size=128, workspace=ws)
+    lora.lora_w4_project(x.clone(), packed, s, want, group_size=128)
+    assert torch.equal(out, want)
+
+
