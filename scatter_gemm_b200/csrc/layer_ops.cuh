@@ -333,19 +333,21 @@ lora_status w4_mv(const lora::W4Args& a, int sms, cudaStream_t st) {
   return launch_status();
 }
 
-// Clusters of 1 .. 8 blocks of one SM each that the current device holds at
+// Clusters of 1 .. 8 blocks of a kernel, one block an SM, that a device holds at
 // once (fewer than its SMs over the size, where that does not divide a GPC's).
 struct ClusterFacts {
   std::atomic<int> ready{0};
   int most[9] = {0};
 };
-ClusterFacts g_clusters[kMaxDevices];
 
+// The current device's of a kernel's facts (one for each device), which how a
+// tile's K is split goes by: null where one cannot be asked for, to be asked for
+// again by the next call.
 template <class K>
-const int* cluster_counts(K kernel, int threads, size_t smem) {
+const int* cluster_counts(ClusterFacts* facts, K kernel, int threads, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  ClusterFacts& f = g_clusters[dev];
+  ClusterFacts& f = facts[dev];
   if (f.ready.load(std::memory_order_acquire)) return f.most;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   if (!f.ready.load(std::memory_order_relaxed)) {
@@ -357,9 +359,10 @@ const int* cluster_counts(K kernel, int threads, size_t smem) {
       LaunchAttrs la;
       la.cluster(cs);
       la.apply(cfg);
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) f.most[cs] = n;
-      cudaGetLastError();  // a failed query must not leave a sticky launch error
+      if (cudaOccupancyMaxActiveClusters(&f.most[cs], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a failed query must not leave a sticky launch error
+        return nullptr;
+      }
     }
     f.ready.store(1, std::memory_order_release);
   }
@@ -395,7 +398,8 @@ lora_status w4_tc(const lora::W4Args& a, int sms, cudaStream_t st) {
   if (!set_smem_once(ready, reinterpret_cast<const void*>(kernel), kW4Smem,
                      C::kSplit ? C::kRegs : 0))
     return LORA_ERR_CUDA;
-  const int* most = cluster_counts(kernel, C::kThreads, smem);
+  static ClusterFacts facts[kMaxDevices];
+  const int* most = cluster_counts(facts, kernel, C::kThreads, smem);
   if (!most) return LORA_ERR_CUDA;
   // Whole waves of one tile for each SM; the tiles left over share the SMs by
   // splitting their K range over clusters, in a launch of their own that takes

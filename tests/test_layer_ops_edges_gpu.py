@@ -2,6 +2,10 @@
 formulas in 64 bits: the values of 8-bit outputs, the range of the element
 types, infinities, and the kernel variants that serve prompts.  Tolerances as
 in test_layer_ops_gpu.py."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -11,6 +15,7 @@ from tests.test_layer_ops_gpu import (DT, E4M3, HALF, SENT, TINY, check_norm, ch
                                       w4_inputs, within)
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
@@ -166,5 +171,40 @@ def test_w4_longest_rows_off_the_grid_take_a_given_workspace(tok):
     lora.lora_w4_project(x, packed, s, out, group_size=128, workspace=ws)
     lora.lora_w4_project(x.clone(), packed, s, want, group_size=128)
     assert torch.equal(out, want)
+
+
+FIRST_CALLS = r"""
+import hashlib, sys, torch
+from scatter_gemm_b200 import lora
+from tests.test_layer_ops_gpu import w4_inputs
+captured = sys.argv[1] == "captured"
+got = {}
+for tok in eval(sys.argv[2]):
+    x, _, _, packed, s, _ = w4_inputs(tok, tok, 2048, 1024, "bf16", 128, False, False)
+    out = torch.zeros(tok, 1024, dtype=x.dtype, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    if captured:
+        with torch.cuda.graph(graph):
+            lora.lora_w4_project(x, packed, s, out, group_size=128)
+        graph.replay()
+    else:
+        lora.lora_w4_project(x, packed, s, out, group_size=128)
+    got[tok] = hashlib.sha1(out.view(torch.int16).cpu().numpy().tobytes()).hexdigest()
+assert lora.device_error() == 0
+print(sorted(got.items()))
+"""
+
+
+def test_w4_results_do_not_depend_on_the_calls_before():
+    # nor on whether a kernel's first call is a captured one
+    said = set()
+    for how, order in (("plain", [4, 12, 40, 60, 300]), ("plain", [300, 60, 40, 12, 4]),
+                       ("captured", [40, 300, 4, 12, 60])):
+        r = subprocess.run([sys.executable, "-c", FIRST_CALLS, how, str(order)], cwd=ROOT, text=True,
+                           capture_output=True, timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
+        said.add(r.stdout)
+    assert len(said) == 1
 
 
