@@ -51,7 +51,7 @@ void launch_rmsnorm(const lora::RmsNormArgs& a, int T, cudaStream_t st) {
 }
 
 template <class E, bool AL>
-lora_status rmsnorm(lora::RmsNormArgs a, cudaStream_t st) {
+lora_status rmsnorm(lora::RmsNormArgs a, int sms, cudaStream_t st) {
   // a row cut at x's 16-byte boundaries may take one block more than its
   // length; the widest rows have no thread for it and are cut at their start
   a.follow = (a.H + 14) / 8 <= 8 * 1024;
@@ -61,7 +61,7 @@ lora_status rmsnorm(lora::RmsNormArgs a, cudaStream_t st) {
   // (8192 x 5120: 60 us with up to 256, 65 with 512, 80 with 1024 threads a
   // row); below that more threads, for the latency of each (777 x 3583: 8.5 us
   // with 512 against 9.4 with 256).
-  const int most = a.tok >= 148 * 8 ? 256 : a.tok >= 148 ? 512 : 1024;
+  const int most = a.tok >= sms * 8 ? 256 : a.tok >= sms ? 512 : 1024;
   int vpt = 1;
   while (vpt < 8 && (blocks + vpt - 1) / vpt > most) vpt *= 2;
   const int T = round_up((blocks + vpt - 1) / vpt, 32);
@@ -108,9 +108,11 @@ extern "C" lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* res
                   rows16(residual_out, ld_res_out) && rows16(weight, 0) && rows16(out, ld_out) &&
                   (!out_q || (aligned_to(out_q, 8) && ld_q % 8 == 0));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const DeviceFacts* dev = device_facts();
+  if (!dev) return LORA_ERR_CUDA;
   if (dtype == LORA_BF16)
-    return al ? rmsnorm<lora::Bf16, true>(a, st) : rmsnorm<lora::Bf16, false>(a, st);
-  return al ? rmsnorm<lora::Fp16, true>(a, st) : rmsnorm<lora::Fp16, false>(a, st);
+    return al ? rmsnorm<lora::Bf16, true>(a, dev->sms, st) : rmsnorm<lora::Bf16, false>(a, dev->sms, st);
+  return al ? rmsnorm<lora::Fp16, true>(a, dev->sms, st) : rmsnorm<lora::Fp16, false>(a, dev->sms, st);
 }
 
 // ------------------------------------------------------------------ rotate and append
@@ -131,13 +133,13 @@ void launch_rope(const lora::RopeAppendArgs& a, int lg, unsigned grid, int parts
 }
 
 template <class E, bool C8, bool INTER, bool NORM>
-lora_status rope_pieces(const lora::RopeAppendArgs& a, cudaStream_t st) {
+lora_status rope_pieces(const lora::RopeAppendArgs& a, int sms, cudaStream_t st) {
   int lg = 4;
   while (lg < a.D / 16) lg *= 2;
   const int all = ((a.hq + 2 * a.hkv) * lg + 31) / 32;  // steps of a token
   // A warp a step as long as the SMs hold most of those warps at once; then as
   // few warps to a token as still fill the SMs.
-  const int64_t warps = 148 * 24;
+  const int64_t warps = static_cast<int64_t>(sms) * 24;
   int parts = all;
   if (static_cast<int64_t>(a.tok) * all > 2 * warps)
     parts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(all, 2 * warps / a.tok)));
@@ -152,7 +154,7 @@ lora_status rope_pieces(const lora::RopeAppendArgs& a, cudaStream_t st) {
 }
 
 template <class E, bool C8>
-lora_status rope_append(const lora::RopeAppendArgs& a, cudaStream_t st) {
+lora_status rope_append(const lora::RopeAppendArgs& a, int sms, cudaStream_t st) {
   const int heads = a.hq + 2 * a.hkv;
   auto mul = [](int64_t m, std::initializer_list<int64_t> v) {
     for (int64_t x : v)
@@ -168,10 +170,10 @@ lora_status rope_append(const lora::RopeAppendArgs& a, cudaStream_t st) {
       aligned_to(a.qw, 16) && aligned_to(a.kw, 16);
   if (pieces) {
     const lora_status s = a.interleaved
-                              ? (a.qw ? rope_pieces<E, C8, true, true>(a, st)
-                                      : rope_pieces<E, C8, true, false>(a, st))
-                              : (a.qw ? rope_pieces<E, C8, false, true>(a, st)
-                                      : rope_pieces<E, C8, false, false>(a, st));
+                              ? (a.qw ? rope_pieces<E, C8, true, true>(a, sms, st)
+                                      : rope_pieces<E, C8, true, false>(a, sms, st))
+                              : (a.qw ? rope_pieces<E, C8, false, true>(a, sms, st)
+                                      : rope_pieces<E, C8, false, false>(a, sms, st));
     if (s != LORA_OK) return s;
   } else {
     const int64_t grid = (static_cast<int64_t>(a.tok) * heads + 7) / 8;
@@ -268,9 +270,12 @@ extern "C" lora_status lora_rope_append(
   a.idx64 = index_bytes == 8;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool c8 = cache_dtype == LORA_E4M3;
+  const DeviceFacts* dev = device_facts();
+  if (!dev) return LORA_ERR_CUDA;
+  const int sms = dev->sms;
   if (dtype == LORA_BF16)
-    return c8 ? rope_append<lora::Bf16, true>(a, st) : rope_append<lora::Bf16, false>(a, st);
-  return c8 ? rope_append<lora::Fp16, true>(a, st) : rope_append<lora::Fp16, false>(a, st);
+    return c8 ? rope_append<lora::Bf16, true>(a, sms, st) : rope_append<lora::Bf16, false>(a, sms, st);
+  return c8 ? rope_append<lora::Fp16, true>(a, sms, st) : rope_append<lora::Fp16, false>(a, sms, st);
 }
 
 // ------------------------------------------------------------------ 4-bit base projection
