@@ -599,7 +599,8 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
         raise ValueError(f"w_scales must be {s_shape}, got {tuple(w_scales.shape)}")
     ptr_z = ptr_sx = 0
     if w_zeros is not None:
-        if _ld(w_zeros, "w_zeros", torch.uint8, s_shape, dev) != ld_s or w_zeros.shape != s_shape:
+        ld_z = _ld(w_zeros, "w_zeros", torch.uint8, s_shape, dev)
+        if w_zeros.shape != s_shape or (ld_z != ld_s and s_shape[0] > 1):
             raise ValueError("w_zeros must have the shape and row stride of w_scales")
         ptr_z = w_zeros.data_ptr()
     if (x_scale is not None) != (x_dt == 2):

@@ -208,3 +208,19 @@ def test_w4_results_do_not_depend_on_the_calls_before():
     assert len(said) == 1
 
 
+def test_w4_one_groups_zeros_of_any_row_stride():
+    x, _, q, packed, s, z = w4_inputs(96, 3, 100, 50, "bf16", 128, True, False)
+    want = torch.empty(3, 50, dtype=x.dtype, device="cuda")
+    lora.lora_w4_project(x, packed, s, want, group_size=128, w_zeros=z)
+    wide = torch.full((2, 70), 0xAB, dtype=torch.uint8, device="cuda")
+    wide[:1, :50] = z
+    got = torch.empty_like(want)
+    lora.lora_w4_project(x, packed, s, got, group_size=128, w_zeros=wide[:1, :50])
+    assert torch.equal(got, want)
+    # with two groups the strides must agree
+    x, _, q, packed, s, z = w4_inputs(97, 3, 200, 50, "bf16", 128, True, False)
+    wide = torch.zeros(2, 70, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        lora.lora_w4_project(x, packed, s, got, group_size=128, w_zeros=wide[:, :50])
+
+
