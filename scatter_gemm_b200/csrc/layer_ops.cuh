@@ -103,10 +103,13 @@ extern "C" lora_status lora_rmsnorm(const void* x, int64_t ld_x, const void* res
                             static_cast<const uint16_t*>(weight), static_cast<uint16_t*>(out),
                             ld_out, static_cast<uint8_t*>(out_q), ld_q, out_scale, tok, H, eps,
                             weight_offset, 0};
-  auto rows16 = [](const void* p, int64_t ld) { return !p || (aligned_to(p, 16) && ld % 8 == 0); };
+  // (the stride of an only row says nothing)
+  auto rows16 = [tok](const void* p, int64_t ld) {
+    return !p || (aligned_to(p, 16) && (tok == 1 || ld % 8 == 0));
+  };
   const bool al = H % 8 == 0 && rows16(x, ld_x) && rows16(residual, ld_res) &&
                   rows16(residual_out, ld_res_out) && rows16(weight, 0) && rows16(out, ld_out) &&
-                  (!out_q || (aligned_to(out_q, 8) && ld_q % 8 == 0));
+                  (!out_q || (aligned_to(out_q, 8) && (tok == 1 || ld_q % 8 == 0)));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const DeviceFacts* dev = device_facts();
   if (!dev) return LORA_ERR_CUDA;
@@ -164,8 +167,9 @@ lora_status rope_append(const lora::RopeAppendArgs& a, int sms, cudaStream_t st)
   const int cb = C8 ? 8 : 16;  // bytes of a piece of the cache
   const bool pieces =
       a.D % 16 == 0 && (a.R % 16 == 0 || a.interleaved) && aligned_to(a.qkv, 16) &&
-      mul(8, {a.ld_qkv, a.off_q, a.off_k, a.off_v, a.ld_q, a.k_page, a.k_slot, a.k_head, a.v_page,
-              a.v_slot, a.v_head}) &&
+      (a.tok == 1 || mul(8, {a.ld_qkv, a.ld_q})) &&  // an only row's stride says nothing
+      mul(8, {a.off_q, a.off_k, a.off_v, a.k_page, a.k_slot, a.k_head, a.v_page, a.v_slot,
+              a.v_head}) &&
       aligned_to(a.q_out, 16) && aligned_to(a.kc, cb) && aligned_to(a.vc, cb) &&
       aligned_to(a.qw, 16) && aligned_to(a.kw, 16);
   if (pieces) {
@@ -523,6 +527,10 @@ extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float*
       !aligned_to(w_scales, 2) || !aligned_to(out, 2))
     return LORA_ERR_INVALID_ARGUMENT;
   if ((workspace_bytes && !workspace) || !aligned_to(workspace, 16)) return LORA_ERR_INVALID_ARGUMENT;
+  const bool x8 = x_dtype == LORA_E4M3;
+  // the stride of an only row says nothing
+  if (tok == 1) ld_x = w4_pitch(K, x8) / (x8 ? 1 : 2);
+  if (N == 1) ld_w = static_cast<int64_t>(K + 31) / 32 * 16;
   if (!aligned_to(W, 16) || ld_w % 16) return LORA_ERR_UNSUPPORTED;
   const lora::W4Args a{x, ld_x, x_scale, static_cast<const uint8_t*>(W), ld_w,
                        static_cast<const uint16_t*>(w_scales), w_zeros, ld_s,
@@ -531,7 +539,6 @@ extern "C" lora_status lora_w4_project(const void* x, int64_t ld_x, const float*
   const DeviceFacts* dev = device_facts();
   if (!dev) return LORA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool x8 = x_dtype == LORA_E4M3;
   if (dtype == LORA_BF16)
     return x8 ? w4_project<lora::Bf16, true>(a, workspace, workspace_bytes, dev->sms, st)
               : w4_project<lora::Bf16, false>(a, workspace, workspace_bytes, dev->sms, st);

@@ -592,8 +592,6 @@ def lora_w4_project(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Ten
     s_shape = (-(-K // group_size), N)
     ld_x = _ld(x, "x", x_dtype, x_shape, dev)
     ld_w = _rows(w_packed, "w_packed", torch.uint8, N, -(-K // 32) * 16, dev)
-    if N == 1:  # a single row of any stride, packed in whole 16-byte blocks
-        ld_w = -(-K // 32) * 16
     ld_s = _ld(w_scales, "w_scales", dtype, s_shape, dev)
     if w_scales.shape != s_shape:
         raise ValueError(f"w_scales must be {s_shape}, got {tuple(w_scales.shape)}")

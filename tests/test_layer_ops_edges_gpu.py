@@ -224,3 +224,43 @@ def test_w4_one_groups_zeros_of_any_row_stride():
         lora.lora_w4_project(x, packed, s, got, group_size=128, w_zeros=wide[:, :50])
 
 
+def test_w4_a_single_row_of_any_stride():
+    # the stride of an only row says nothing: 120000 columns are more than
+    # shared memory holds, so TMA has to take them
+    x, _, q, packed, s, z = w4_inputs(98, 2, 120000, 33, "bf16", 128, False, False, pad=1)
+    assert x.stride(0) % 8
+    out, want = (torch.empty(1, 33, dtype=x.dtype, device="cuda") for _ in range(2))
+    lora.lora_w4_project(x[:1].clone(), packed, s, want, group_size=128)
+    lora.lora_w4_project(x[:1], packed, s, out, group_size=128)
+    assert torch.equal(out, want)
+
+
+def test_one_token_of_any_stride():
+    # norm and rotation of the first row of a padded batch
+    g = gen(99)
+    x = strided(rand(g, 2, 520, dtype=torch.bfloat16), 3)[:1]
+    w = rand(g, 520, dtype=x.dtype)
+    check_norm(x.clone(), w)
+    got, want = new(1, 520, x.dtype), new(1, 520, x.dtype)
+    lora.lora_rmsnorm(x, w, got)
+    lora.lora_rmsnorm(x.clone(), w, want)
+    assert torch.equal(got, want)
+    check_rope(99, 1, 4, 2, 64, pad=3)
+
+
+@pytest.mark.parametrize("tok", [1, 12])
+def test_w4_one_output_of_any_row_stride(tok):
+    x, _, q, packed, s, z = w4_inputs(100, tok, 200, 1, "bf16", 64, True, False)
+    wide = torch.full((2, packed.shape[1] + 7), 0xAB, dtype=torch.uint8, device="cuda")[:1, :packed.shape[1]]
+    wide.copy_(packed)
+    out, want = (torch.empty(tok, 1, dtype=x.dtype, device="cuda") for _ in range(2))
+    lora.lora_w4_project(x, packed, s, want, group_size=64, w_zeros=z)
+    lora.lora_w4_project(x, wide, s, out, group_size=64, w_zeros=z)
+    assert torch.equal(out, want)
+    got = lora.lib().lora_w4_project(
+        x.data_ptr(), 200, None, wide.data_ptr(), wide.stride(0), s.data_ptr(), z.data_ptr(), 1,
+        out.zero_().data_ptr(), 1, tok, 200, 1, 64, 0, 0, None, 0,
+        torch.cuda.current_stream().cuda_stream)
+    assert got == lora.LORA_OK and torch.equal(out, want)
+
+
