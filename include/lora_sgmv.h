@@ -426,7 +426,7 @@ LORA_API lora_status lora_w4_project(const void* x, int64_t ld_x, const float* x
  *                                + h*strides[2], page = s / page_size: rn(k' * rn32(1 / k_scale))
  *                                and rn(v * rn32(1 / v_scale)), as for out_q above; strides
  *                                (HOST, elements) of each cache; cache_dtype is `dtype` or
- *                                LORA_E4M3
+ *                                LORA_E4M3; scales above 2^-128, whose reciprocal is finite
  *   slots    [tok]               the cache slot of each token; a token whose slot is negative
  *                                or at least num_pages*page_size writes no cache entry.
  *                                Slots of one call must differ: of equal ones any token's

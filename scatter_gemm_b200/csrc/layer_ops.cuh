@@ -9,6 +9,7 @@
 #include "w4_tc.cuh"
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <type_traits>
 
@@ -214,7 +215,9 @@ extern "C" lora_status lora_rope_append(
   const int wq = off[1] - off[0], wk = off[2] - off[1], wv = off[3] - off[2];
   if (wq % head_dim || wk % head_dim || wk != wv || ld_q < wq) return LORA_ERR_INVALID_ARGUMENT;
   if ((q_weight != nullptr) != (k_weight != nullptr)) return LORA_ERR_INVALID_ARGUMENT;
-  if (!(k_scale > 0.f) || !(v_scale > 0.f)) return LORA_ERR_INVALID_ARGUMENT;
+  // positive, and with a finite reciprocal, which is what is multiplied by
+  if (!(k_scale > 0.f) || !(v_scale > 0.f) || std::isinf(1.f / k_scale) || std::isinf(1.f / v_scale))
+    return LORA_ERR_INVALID_ARGUMENT;
   if (rotary_dim && (max_pos < 1 || (axes > 1 && (!axis_map || ld_pos < tok))))
     return LORA_ERR_INVALID_ARGUMENT;
   for (int i = 0; i < 3; ++i)
