@@ -264,3 +264,89 @@ def test_w4_one_output_of_any_row_stride(tok):
     assert got == lora.LORA_OK and torch.equal(out, want)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("mode", ["rounded", "both", "8bit"])
+@pytest.mark.parametrize("tok,H,pad", [(1200, 5120, 0), (1300, 8191, 1), (1190, 12000, 3),
+                                       (3, 24576, 0), (2, 32768, 0), (3, 30001, 5),
+                                       (150, 16400, 0), (2, 65536, 0), (2, 65530, 1)])
+def test_norm_of_wide_rows_and_many_rows(tok, H, pad, mode, in_place):
+    # four and eight blocks of eight a thread, up to 256, 512 and 1024 threads a row
+    g = gen(tok + H)
+    x, res = (rand(g, tok, H, dtype=torch.bfloat16, std=s) for s in (1.0, 3.0))
+    w = (1 + rand(g, H, std=0.2)).bfloat16()
+    check_norm(x, w, res, mode=mode, pad=pad, in_place=in_place)
+
+
+@pytest.mark.parametrize("tok,H,pad", [(1200, 5120, 0), (1300, 8191, 1), (2, 65536, 0), (2, 40000, 1)])
+def test_norm_written_over_x(tok, H, pad):
+    g = gen(tok * H)
+    x, res = (rand(g, tok, H, dtype=torch.float16) for _ in range(2))
+    w = rand(g, H, dtype=torch.float16)
+    want, want_r = strided(x, pad), strided(res, pad)
+    lora.lora_rmsnorm(strided(x, pad), w, want, residual=want_r)
+    a, b = strided(x, pad), strided(res, pad)
+    lora.lora_rmsnorm(a, w, a, residual=b)           # out over x, the stream over the residual
+    assert torch.equal(a, want) and torch.equal(b, want_r)
+    a, out = strided(x, pad), new(tok, H, x.dtype, pad)
+    lora.lora_rmsnorm(a, w, out, residual=res, residual_out=a)   # the stream over x
+    assert torch.equal(out, want) and torch.equal(a, want_r)
+
+
+PROMPT_ROPE = [
+    dict(tok=1500, hq=18, hkv=2, D=128),                       # a step that holds two heads of four
+    dict(tok=1500, hq=18, hkv=2, D=128, norm=True, w0=1.0),
+    dict(tok=1501, hq=37, hkv=3, D=64, c8=True, norm=True),
+    dict(tok=1499, hq=37, hkv=3, D=64, R=32, inter=True),
+    dict(tok=1507, hq=20, hkv=4, D=80, R=40, inter=True, page=7),
+    dict(tok=1507, hq=21, hkv=4, D=80, c8=True, idx=torch.int32),
+    dict(tok=1502, hq=9, hkv=2, D=256, norm=True),
+    dict(tok=1502, hq=9, hkv=2, D=256, c8=True, inter=True, norm=True),
+    dict(tok=1503, hq=5, hkv=1, D=512),
+    dict(tok=1503, hq=5, hkv=1, D=512, norm=True, c8=True),
+    dict(tok=1504, hq=12, hkv=4, D=128, hnd=True, in_place=True),
+    dict(tok=1504, hq=12, hkv=4, D=128, norm=True, in_place=True, inter=True),
+    dict(tok=8200, hq=5, hkv=1, D=128),
+    dict(tok=8200, hq=7, hkv=2, D=64, norm=True, c8=True),
+    dict(tok=8200, hq=3, hkv=1, D=96, R=48, inter=True, norm=True),
+]
+
+
+@pytest.mark.parametrize("kw", PROMPT_ROPE)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_rope_prompts(kw, dtype):
+    # several steps of heads a warp, two under way, the last ones partly filled
+    kw = dict(kw)
+    args = [kw.pop(n) for n in ("tok", "hq", "hkv", "D")]
+    check_rope(100 + args[0], *args, dtype, **kw)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("sections,mixed", [([24, 20, 20], True), ([16, 24, 24], False), ([32, 32], False)])
+def test_rope_prompts_of_several_axes(sections, mixed, norm):
+    amap = lora.rope_axis_map(sections, interleaved=mixed)
+    check_rope(101, 1600, 14, 4, 128, axes=len(sections), amap=amap, norm=norm)
+    check_rope(102, 8195, 3, 1, 128, axes=len(sections), amap=amap, norm=norm, c8=True)
+
+
+@pytest.mark.parametrize("tok", [5, 1500])
+@pytest.mark.parametrize("D", [33, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_rope_scaled_cache_of_16_bits(dtype, D, tok):
+    dt, hq, hkv = DT[dtype], 9, 3
+    g = gen(103)
+    off = [0, hq * D, (hq + hkv) * D, (hq + 2 * hkv) * D]
+    qkv, R = rand(g, tok, off[3], dtype=dt), D // 2 * 2
+    cs = rand(g, 50, R).clamp(-1, 1)
+    pos = torch.randint(0, 50, (tok,), generator=g, device="cuda")
+    kc, vc = (torch.full((tok, 1, hkv, D), SENT, device="cuda").to(dt) for _ in range(2))
+    slots = torch.randperm(tok, generator=g, device="cuda")
+    q = torch.empty(tok, hq * D, dtype=dt, device="cuda")
+    lora.lora_rope_append(qkv, off, D, pos, cs, kc, vc, slots, q_out=q, k_scale=0.7, v_scale=1.9)
+    rq, rk, rv, mq, mk = rope_ref(qkv, off, D, pos, cs, R, None, False, None, None, 1e-6, 0.0)
+    within(q.reshape(rq.shape), rq, rq.abs() * HALF[dt] + mq * 2.0 ** -22 + TINY[dt], "q")
+    # the scale and its reciprocal in fp32, and two products: 2^-21
+    for c, ref, mag, sc in ((kc, rk, mk, 0.7), (vc, rv, rv.abs(), 1.9)):
+        ref, mag = ref / sc, mag / sc
+        within(c[slots, 0], ref, ref.abs() * HALF[dt] + mag * 2.0 ** -21 + TINY[dt], "cache")
+
+
