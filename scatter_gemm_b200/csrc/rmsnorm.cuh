@@ -15,8 +15,13 @@
 // (the sum, then the outputs), so each input is read once and each output
 // written once: the bound is the memory traffic, 2 bytes for each of x,
 // residual, h and out and 1 for q.  8192 x 5120 with all of them: 59.8 us, 6.3
-// TB/s, 96 % of the measured copy rate; one row of 4096: 1.9 us.  (Rows of more
-// than 32,768 elements hold 64 values a thread and spill.)
+// TB/s, 96 % of the measured copy rate; one row of 4096: 1.9 us.
+// Every variant may have 1024 threads a row, hence 64 registers a thread.  Rows
+// of eight blocks of eight a thread spill there, 212 bytes a thread or 340 with q,
+// off the 16-byte grid 1028 or 1164: those of more than 8192 elements with many
+// rows (eight for each SM), of more than 16,384 with a row for each SM, of more
+// than 32,768 else.  2560 x 16384 with all outputs takes 95 us, 2560 x 16383 157,
+// where the traffic alone would take 58.  (Four blocks off the grid: 24, 40 bytes.)
 #pragma once
 
 #include <cuda_fp8.h>

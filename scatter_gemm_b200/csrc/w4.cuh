@@ -221,7 +221,8 @@ struct MvBlock {
 // 22.6 us for 8 tokens (7.7 against 8.5 us for one token at 4096 x 6144).  At
 // 4096 x 24576 one token takes 19 us, 2.7 TB/s, where the weights' 52 MB alone
 // would take 8: about 5 us are start-up and end, and then the bound is what
-// four warps a scheduler issue, some 170 instructions for each KB of weights.
+// four warps a scheduler issue, some 210 instructions for each KB of weights, 240
+// with eight tokens.
 // Weights by 8, 16 or 32 rows a warp, deeper prefetch, or three and four
 // smaller blocks an SM were all within 5 % of this.
 //

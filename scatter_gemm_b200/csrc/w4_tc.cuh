@@ -29,8 +29,11 @@
 //
 // 2048 tokens x 5120 x 7168: 148 us, 1.01 PFLOP/s, the tensor pipe 50 % and the
 // issue slots 72 % busy: a block of 128 tokens takes some 2,900 warp
-// instructions where the tensor pipe's 512 cycles have 2,048 slots.  9 tokens x
-// 4096 x 6144: 10.7 us; 64 tokens: 14.3 us.
+// instructions where the tensor pipe's 512 cycles have 2,048 slots.  With groups
+// of 64 and 32, two and four accumulators a block: 211 and 360 us; with 8-bit x
+// 157, and 446 with groups of 32 (128 tokens of 8-bit x in groups of 64 or 32
+// spill 32 to 34 bytes a thread, 32 tokens 8, or 20 of 16-bit x in groups of
+// 128).  9 tokens x 4096 x 6144: 10.7 us; 64 tokens: 14.3 us.
 #pragma once
 
 #include "common.cuh"
