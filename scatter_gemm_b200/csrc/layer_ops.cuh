@@ -322,7 +322,7 @@ inline bool w4_mv_holds(int tok, int K) {
 // Whether rows of x that TMA cannot load are copied to rows that it can (where
 // there is a workspace): from 17 tokens on, and where w4_mv would read the
 // weights more than once (13 x 8191 x 6144, twice: 37.9 us, copied 21.5).  Where
-// it reads them once it is the faster (13 x 3583 x 6159: 16.5, copied 18.2).
+// it reads them once it is the faster (13 x 3583 x 6159: 16, copied 18).
 inline bool w4_copies(int tok, int K) { return tok > 16 || !w4_mv_holds(tok, K); }
 
 template <class E, bool X8, int NT, int VW>

@@ -478,6 +478,10 @@ w4_mv_kernel(const W4Args p, const int tt) {
               w4_mma<C>(g1[n], p1, q1, p3, q3, xv.z, xv.w, false);
           }
         }
+        // a group behind K was given the last one's scale, which may be infinite;
+        // its sums are 0 (to load nothing there instead took 14.7 against 11.4 us
+        // for 4 tokens x 4096 x 6144 in groups of 32)
+        if (kSub > 1 && blk * kSub + sub > last_g) sz0 = sz1 = 0;
         const float s0 = E::bits_to_f32(static_cast<uint16_t>(sz0));
         const float s1 = E::bits_to_f32(static_cast<uint16_t>(sz1));
 #pragma unroll

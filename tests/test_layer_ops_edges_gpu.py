@@ -54,6 +54,24 @@ def test_rope_cache_values_are_products_with_the_rounded_reciprocal(tok, D, c8):
         assert torch.equal(c.float().reshape(tok, -1), want.float())
 
 
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("K,group", [(40, 32), (70, 64), (200, 32), (130, 128), (300, 64)])
+@pytest.mark.parametrize("tok", [1, 8, 20, 100])
+def test_w4_infinite_scale_of_the_last_group(tok, K, group, x8):
+    # the groups that would follow behind K add nothing, whatever that scale
+    x, sx, q, packed, s, z = w4_inputs(104, tok, K, 50, "bf16", group, True, x8)
+    s[-1, 7], s[-1, 30] = float("inf"), float("-inf")
+    out = new(tok, 50, torch.bfloat16)
+    lora.lora_w4_project(x, packed, s, out, group_size=group, w_zeros=z, x_scale=sx)
+    g0 = (-(-K // group) - 1) * group
+    last = x[:, g0:].double() @ (q[:, g0:].double() - z[-1].double()[:, None]).T
+    for col, sign in ((7, 1.0), (30, -1.0)):
+        want = last[:, col] * sign * float("inf")  # NaN where the group's sum is 0
+        assert torch.equal(out[:, col].double().nan_to_num(7.0), want.nan_to_num(7.0))
+    out[:, [7, 30]] = 0
+    assert out.isfinite().all()
+
+
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("tok,lead", [(1, 0), (5, 0), (8, 0), (9, 0), (13, 1), (40, 0)])
 def test_w4_range_of_bf16_x(tok, lead, zeros):
