@@ -322,7 +322,9 @@ inline bool w4_mv_holds(int tok, int K) {
 // Whether rows of x that TMA cannot load are copied to rows that it can (where
 // there is a workspace): from 17 tokens on, and where w4_mv would read the
 // weights more than once (13 x 8191 x 6144, twice: 37.9 us, copied 21.5).  Where
-// it reads them once it is the faster (13 x 3583 x 6159: 16, copied 18).
+// it reads them once it is the faster with small groups (13 x 3583 x 6159 in
+// groups of 32: 16, copied 18) and about even with large ones (13 x 3583, groups
+// of 128, 6144 and 24,576 wide: 12.9 and 26.0, copied some 12.3 and 25.5).
 inline bool w4_copies(int tok, int K) { return tok > 16 || !w4_mv_holds(tok, K); }
 
 template <class E, bool X8, int NT, int VW>
